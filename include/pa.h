@@ -57,6 +57,7 @@ typedef enum pa_status {
 #define PA_ERRBIT_COPY 0x8u      /* block copy: a src/dst id outside [0, num_blocks)           */
 #define PA_ERRBIT_TOKEN 0x10u    /* slot map: sequence, position or table entry out of range   */
 #define PA_ERRBIT_TIMEOUT 0x20u  /* a kernel's bounded wait on its own copies gave up          */
+#define PA_ERRBIT_POOL 0x40u     /* table build: the free list holds too few blocks            */
 
 /*
  * Bytes of device scratch pa_decode needs for this batch shape.  The decode
@@ -539,6 +540,138 @@ pa_status pa_slot_mapping(int64_t* slot_mapping, const int32_t* block_tables,
                           int max_blocks_per_seq, const int32_t* token_seq,
                           const int32_t* token_pos, int num_tokens, int num_seqs, int block_size,
                           int num_blocks, pa_stream_t stream);
+
+/*
+ * Block tables, context lengths, query starts and the slot map of one step,
+ * built on the GPU from request lengths [P1 §3.2-§3.3: a sequence takes a
+ * block when its last one is full, and the free list pops its last entry;
+ * P2 §2.3 address map; P3 §2.3: a shared prefix is one set of blocks in
+ * several tables].  It replaces the host's bookkeeping of a step, so a decode
+ * loop can run as one graph.  With c_s = cached_lens[s] + new_lens[s]:
+ *
+ *   held_s = ceil(cached_lens[s] / B), or the group's shared blocks if more
+ *   need_s = max(0, ceil(c_s / B) - held_s)
+ *   block_tables[s][held_s + k] = free_list[num_free - 1 - (sum of need before s) - k],  k < need_s
+ *   context_lens[s] = c_s
+ *   query_start[s]  = sum of new_lens before s          (query_start[num_seqs]: the total)
+ *   slot_mapping[query_start[s] + i] = block_tables[s][p / B] * B + p % B,  p = cached_lens[s] + i
+ *   num_free_out    = num_free - sum of need
+ *
+ * Groups share a prefix: the sequences [group_start[g], group_start[g+1])
+ * have the same prefix_blocks[g] leading blocks.  Those entries of every
+ * member are copied from the group's first sequence (which may be taking
+ * them in this very call); the others take blocks only past them.  A
+ * member's new tokens at positions inside the shared blocks get slot -1: the
+ * first sequence writes them.  Sequences outside every group share nothing.
+ *
+ *   block_tables   int32 [num_seqs][max_blocks_per_seq]: the entries of the
+ *                  shared and of the new blocks are written, the others left
+ *   context_lens   int32 [num_seqs] (written); may be cached_lens itself
+ *   query_start    int32 [num_seqs + 1] (written)
+ *   slot_mapping   int64 [num_slots] (written); entries past the last new
+ *                  token are -1 (padding), so num_slots may be the fixed
+ *                  length of a captured step
+ *   num_free_out   int32 [1] (written); may be num_free itself
+ *   free_list      int32 [free_list_len]; its first *num_free entries are free
+ *   num_free       int32 [1], on the device
+ *   cached_lens, new_lens   int32 [num_seqs]
+ *   group_start    int32 [num_groups + 1], increasing, or NULL with num_groups == 0
+ *   prefix_blocks  int32 [num_groups], or NULL with num_groups == 0
+ *   workspace      pa_build_tables_workspace_size(num_seqs) bytes, 16-byte
+ *                  aligned; contents ignored.  Calls that share one must not
+ *                  overlap on the GPU.
+ * The arrays written must not overlap each other or, but for the two cases
+ * above, the arrays read; the same pointer in two places returns
+ * PA_ERR_INVALID_ARG.  Errors found on the device:
+ *   - too few free blocks (or *num_free outside [0, free_list_len], or 2^31
+ *     new tokens): PA_ERRBIT_POOL, and the call does what it would do if
+ *     every new length were 0: no block is taken, lengths stay;
+ *   - a negative length or one past the table: PA_ERRBIT_CONTEXT, and that
+ *     sequence gets no new tokens (its cached length is clipped);
+ *   - prefix_blocks[g] below 0 or above the blocks of the group's first
+ *     sequence: PA_ERRBIT_CONTEXT, clipped.  A group whose bounds are not
+ *     0 <= start < end <= num_seqs shares nothing;
+ *   - more new tokens than num_slots: PA_ERRBIT_TOKEN; the slots that exist
+ *     are written.  A block id outside [0, num_blocks) gives slot -1 and the
+ *     same bit.
+ * num_seqs * max_blocks_per_seq must be below 2^31 (else PA_ERR_UNSUPPORTED).
+ */
+size_t pa_build_tables_workspace_size(int num_seqs);
+pa_status pa_build_tables(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens,
+                          int32_t* query_start, int64_t* slot_mapping, int num_slots,
+                          int32_t* num_free_out, const int32_t* free_list, int free_list_len,
+                          const int32_t* num_free, const int32_t* cached_lens,
+                          const int32_t* new_lens, const int32_t* group_start,
+                          const int32_t* prefix_blocks, int num_groups, int num_seqs,
+                          int block_size, int num_blocks, void* workspace, size_t workspace_bytes,
+                          pa_stream_t stream);
+
+/* ---- Latent cache --------------------------------------------------------
+ * Latent attention caches one row a token for all heads: latent_dim values
+ * from which every head's key and value are projections, and rope_dim rotary
+ * key values.  In absorbed form the projections are folded into the query and
+ * the output, so a token's key is its whole row and its value the row's first
+ * latent_dim entries.  The cache is fp16 [num_blocks][block_size][latent_dim +
+ * rope_dim], reached through the same block tables and slots as the caches
+ * above (pa_slot_mapping, pa_build_tables, pa_swap_blocks apply as they are).
+ * Supported: latent_dim 512, rope_dim 64 (else PA_ERR_UNSUPPORTED).  Not part
+ * of the pages: the formula is the ordinary attention of [P2 §2.1].
+ */
+
+/*
+ * Cache write of latent rows: token t's row goes to slot slot_mapping[t],
+ *
+ *   cache[slot / B][slot % B][:] = (latent[t][:], rope[t][:])
+ *
+ * with the slot rules of pa_reshape_and_cache (negative: skipped; past the
+ * pool: skipped and PA_ERRBIT_SLOT).  Bit-exact copy.
+ *
+ *   latent         fp16 [num_tokens][latent_dim], rows latent_stride values apart
+ *   rope           fp16 [num_tokens][rope_dim], rows rope_stride values apart;
+ *                  both may be parts of one projection's output (strides are
+ *                  multiples of 8, at least the row)
+ *   cache          fp16 [num_blocks][block_size][latent_dim + rope_dim] (updated)
+ */
+pa_status pa_latent_write(const void* latent, int64_t latent_stride, const void* rope,
+                          int64_t rope_stride, void* cache, const int64_t* slot_mapping,
+                          int num_tokens, int latent_dim, int rope_dim, int block_size,
+                          int num_blocks, pa_stream_t stream);
+
+/*
+ * Single-token attention over the latent cache in absorbed form:
+ *
+ *   out[s,h,:] = softmax( scale * query[s,h,:] . row_i for i < c_s ) . row_i[0:latent_dim]
+ *
+ * with row_i = cache[block_tables[s][i / B]][i % B][:] and c_s =
+ * context_lens[s].  A sequence with c_s == 0 gets zero rows.
+ *
+ *   out            fp16 [num_seqs][num_heads][latent_dim]              (written)
+ *   query          fp16 [num_seqs][num_heads][latent_dim + rope_dim]
+ *   cache          fp16 [num_blocks][block_size][latent_dim + rope_dim]
+ *   block_tables, context_lens, max_context_len, and the errors found on the
+ *                  device: as for pa_decode (a bad block id reads as zeros)
+ *   scale          multiplier of q.row (normally 1/sqrt of the head's own key size)
+ *   workspace      pa_latent_decode_workspace_size(...) bytes, 16-byte
+ *                  aligned; contents ignored.  Calls that share one must not
+ *                  overlap on the GPU.
+ *
+ * Arithmetic: fp16 products with fp32 accumulation on the tensor cores; the
+ * softmax in fp32, its weights rounded once to fp16 (the sum adds the rounded
+ * weights); partial results in fp32; the result rounded once to fp16.  The
+ * context is split among SMs by the whole batch's lengths, so the last bits
+ * of a sequence's result may depend on the other sequences; the same call
+ * gives the same bits.
+ * Supported: block_size in {8, 16, 32}, num_heads <= 1024, num_blocks *
+ * block_size < 2^31 - 64.  Batches of more than 1024 sequences take a pair of
+ * launches for each 1024.
+ */
+size_t pa_latent_decode_workspace_size(int num_seqs, int num_heads);
+pa_status pa_latent_decode(void* out, const void* query, const void* cache,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, int num_seqs, int num_heads,
+                           int latent_dim, int rope_dim, int block_size, int num_blocks,
+                           float scale, int max_context_len, void* workspace,
+                           size_t workspace_bytes, pa_stream_t stream);
 
 /*
  * Synchronises `stream`, then reads and clears the calling device's error

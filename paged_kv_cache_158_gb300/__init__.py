@@ -86,9 +86,24 @@ _lib.pa_swap_blocks.restype = _i32
 _lib.pa_copy_blocks_fp8.argtypes = [_vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _vp]
 _lib.pa_copy_blocks_fp8.restype = _i32
 
+_i64 = ctypes.c_int64
+_lib.pa_build_tables_workspace_size.argtypes = [_i32]
+_lib.pa_build_tables_workspace_size.restype = _sz
+_lib.pa_build_tables.argtypes = [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                                 _i32, _i32, _i32, _i32, _vp, _sz, _vp]
+_lib.pa_build_tables.restype = _i32
+_lib.pa_latent_write.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp]
+_lib.pa_latent_write.restype = _i32
+_lib.pa_latent_decode_workspace_size.argtypes = [_i32, _i32]
+_lib.pa_latent_decode_workspace_size.restype = _sz
+_lib.pa_latent_decode.argtypes = [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32,
+                                  _i32, _vp, _sz, _vp]
+_lib.pa_latent_decode.restype = _i32
+
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_OUT_OF_RANGE, PA_ERR_TIMEOUT = range(6)
 PA_ERRBIT_BLOCK_ID, PA_ERRBIT_CONTEXT, PA_ERRBIT_SLOT = 0x1, 0x2, 0x4
 PA_ERRBIT_COPY, PA_ERRBIT_TOKEN, PA_ERRBIT_TIMEOUT = 0x8, 0x10, 0x20
+PA_ERRBIT_POOL = 0x40
 PA_DECODE_ZEROED_WORKSPACE = 0x1
 PA_DECODE_INPUTS_READY = 0x2
 PA_PREFILL_INPUTS_READY = 0x2
@@ -488,6 +503,131 @@ def pa_slot_mapping(slot_mapping: torch.Tensor, block_tables: torch.Tensor, toke
     _check(st, "pa_slot_mapping")
 
 
+def _same_device(*tensors) -> None:
+    """The library launches on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def pa_build_tables_workspace_size(num_seqs: int) -> int:
+    return int(_lib.pa_build_tables_workspace_size(num_seqs))
+
+
+def build_tables_workspace(num_seqs: int, device=None) -> torch.Tensor:
+    """A device byte buffer of pa_build_tables_workspace_size(num_seqs) bytes."""
+    return torch.empty(max(pa_build_tables_workspace_size(num_seqs), 16), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def pa_build_tables(block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
+                    slot_mapping: torch.Tensor, num_free_out: torch.Tensor, free_list: torch.Tensor,
+                    num_free: torch.Tensor, cached_lens: torch.Tensor, new_lens: torch.Tensor,
+                    block_size: int, num_blocks: int, workspace: torch.Tensor,
+                    group_start: torch.Tensor | None = None,
+                    prefix_blocks: torch.Tensor | None = None, stream=None) -> None:
+    """Block tables, context lengths, query starts and slot map of a step from the cached and new
+    lengths [S], taking blocks from the end of free_list[:num_free]; sequences of a group share
+    its leading prefix_blocks (see pa_build_tables in include/pa.h).  context_lens may be
+    cached_lens and num_free_out may be num_free."""
+    S = cached_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or \
+            new_lens.shape != (S,) or query_start.shape != (S + 1,) or slot_mapping.dim() != 1 or \
+            free_list.dim() != 1 or num_free.numel() != 1 or num_free_out.numel() != 1:
+        raise ValueError("shape mismatch")
+    if (group_start is None) != (prefix_blocks is None):
+        raise ValueError("group_start and prefix_blocks go together")
+    G = 0
+    if prefix_blocks is not None:
+        G = prefix_blocks.shape[0]
+        if group_start.shape != (G + 1,):
+            raise ValueError("group_start must be [num_groups + 1]")
+    _same_device(block_tables, context_lens, query_start, slot_mapping, num_free_out, free_list,
+                 num_free, cached_lens, new_lens, workspace, group_start, prefix_blocks)
+    st = _lib.pa_build_tables(_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+                              _ptr(context_lens, "context_lens", torch.int32),
+                              _ptr(query_start, "query_start", torch.int32),
+                              _ptr(slot_mapping, "slot_mapping", torch.int64), slot_mapping.shape[0],
+                              _ptr(num_free_out, "num_free_out", torch.int32),
+                              _ptr(free_list, "free_list", torch.int32), free_list.shape[0],
+                              _ptr(num_free, "num_free", torch.int32),
+                              _ptr(cached_lens, "cached_lens", torch.int32),
+                              _ptr(new_lens, "new_lens", torch.int32),
+                              _ptr(group_start, "group_start", torch.int32) if G else None,
+                              _ptr(prefix_blocks, "prefix_blocks", torch.int32) if G else None, G, S,
+                              int(block_size), int(num_blocks),
+                              _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
+                              _stream(stream))
+    _check(st, "pa_build_tables")
+
+
+def _rows_ptr(t: torch.Tensor, name: str) -> int:
+    """fp16 rows whose values are adjacent; the rows may be apart (a slice of a wider array)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name} must be [T, n] with adjacent values")
+    return t.data_ptr()
+
+
+def pa_latent_write(latent: torch.Tensor, rope: torch.Tensor, cache: torch.Tensor,
+                    slot_mapping: torch.Tensor, stream=None) -> None:
+    """Scatter latent rows (latent [T,512], rope [T,64]; either may be a slice of a wider array)
+    into their slots of the latent cache [NB,B,576] (see pa_latent_write in include/pa.h)."""
+    T, L = latent.shape
+    R = rope.shape[1]
+    NB, B, W = cache.shape
+    if rope.shape[0] != T or W != L + R or slot_mapping.shape != (T,):
+        raise ValueError("shape mismatch")
+    _same_device(latent, rope, cache, slot_mapping)
+    st = _lib.pa_latent_write(_rows_ptr(latent, "latent"), latent.stride(0) if T > 1 else L,
+                              _rows_ptr(rope, "rope"), rope.stride(0) if T > 1 else R,
+                              _ptr(cache, "cache", torch.float16),
+                              _ptr(slot_mapping, "slot_mapping", torch.int64), T, L, R, B, NB,
+                              _stream(stream))
+    _check(st, "pa_latent_write")
+
+
+def pa_latent_decode_workspace_size(num_seqs: int, num_heads: int) -> int:
+    return int(_lib.pa_latent_decode_workspace_size(num_seqs, num_heads))
+
+
+def latent_decode_workspace(num_seqs: int, num_heads: int, max_context_len: int | None = None,
+                            device=None) -> torch.Tensor:
+    """A device byte buffer of pa_latent_decode_workspace_size(...) bytes.  (Its size does not
+    depend on the context length; the argument is there for symmetry with decode_workspace.)"""
+    n = pa_latent_decode_workspace_size(num_seqs, num_heads)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_latent_decode(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                     max_context_len: int, workspace: torch.Tensor, stream=None) -> None:
+    """out[S,H,512] = absorbed latent attention of query[S,H,576] over the paged latent cache
+    [NB,B,576] (see pa_latent_decode in include/pa.h)."""
+    S, H, W = query.shape
+    NB, B, W2 = cache.shape
+    L = out.shape[2]
+    if W2 != W or tuple(out.shape) != (S, H, L) or block_tables.dim() != 2 or \
+            block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("shape mismatch")
+    _same_device(out, query, cache, block_tables, context_lens, workspace)
+    st = _lib.pa_latent_decode(_ptr(out, "out", torch.float16), _ptr(query, "query", torch.float16),
+                               _ptr(cache, "cache", torch.float16),
+                               _ptr(block_tables, "block_tables", torch.int32),
+                               block_tables.shape[1],
+                               _ptr(context_lens, "context_lens", torch.int32), S, H, L, W - L, B, NB,
+                               float(scale), int(max_context_len),
+                               _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
+                               _stream(stream))
+    _check(st, "pa_latent_decode")
+
+
 def pa_selftest_wait_timeout(stream=None) -> None:
     """Launches a kernel whose bounded wait never completes (see pa_selftest_wait_timeout in
     include/pa.h): about a second later the device error word holds PA_ERRBIT_TIMEOUT."""
@@ -513,7 +653,8 @@ __all__ = [
     "pa_decode_fp8", "pa_reshape_and_cache_fp8", "pa_copy_blocks_fp8", "pa_convert_cache_fp8",
     "pa_swap_blocks", "pa_prefill", "pa_prefill_fp8", "pa_decode_noalloc", "pa_decode_ex",
     "pa_decode_fp8_ex", "pa_decode_append", "pa_decode_append_fp8", "pa_prefill_ex",
-    "pa_prefill_fp8_ex",
+    "pa_prefill_fp8_ex", "pa_build_tables", "pa_build_tables_workspace_size", "build_tables_workspace",
+    "pa_latent_write", "pa_latent_decode", "pa_latent_decode_workspace_size", "latent_decode_workspace",
     "pa_status_string", "pa_decode_workspace_size", "pa_decode_partition_tokens",
     "pa_decode_set_partition_tokens", "decode_workspace", "raise_on_device_errors", "PAError",
 ]

@@ -180,6 +180,12 @@ int part_tokens_for(int num_seqs, int num_heads, int max_context_len) {
   return items512 < kSmallBatchItems ? 256 : 512;
 }
 
+// Workspaces that hold one entry for each SM's worker are sized for this many
+// (their size is a pure function of the batch, so it can be asked without a
+// device); a call uses at most as many.
+constexpr int kWorkspaceSms = 160;
+constexpr int kMaxLatentHeads = 1024;
+
 struct WsLayout {
   int part_tokens;
   int max_parts;
@@ -669,6 +675,158 @@ pa_status pa_slot_mapping(int64_t* slot_mapping, const int32_t* block_tables,
   return pa::launch_slot_mapping(slot_mapping, block_tables, max_blocks_per_seq, token_seq,
                                  token_pos, num_tokens, num_seqs, block_size, num_blocks, ds.err,
                                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+size_t pa_build_tables_workspace_size(int num_seqs) {
+  return num_seqs < 0 ? 0 : round256(256 + (size_t)num_seqs * (sizeof(int4) + sizeof(int)));
+}
+
+pa_status pa_build_tables(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens,
+                          int32_t* query_start, int64_t* slot_mapping, int num_slots,
+                          int32_t* num_free_out, const int32_t* free_list, int free_list_len,
+                          const int32_t* num_free, const int32_t* cached_lens,
+                          const int32_t* new_lens, const int32_t* group_start,
+                          const int32_t* prefix_blocks, int num_groups, int num_seqs,
+                          int block_size, int num_blocks, void* workspace, size_t workspace_bytes,
+                          pa_stream_t stream) {
+  if (!block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+  if (max_blocks_per_seq <= 0 || num_slots < 0 || free_list_len < 0 || num_groups < 0 ||
+      num_seqs < 0 || num_blocks <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (!query_start || !num_free_out || !num_free || !aligned4(query_start) ||
+      !aligned4(num_free_out) || !aligned4(num_free))
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!block_tables || !context_lens || !cached_lens || !new_lens ||
+                       !aligned4(block_tables) || !aligned4(context_lens) ||
+                       !aligned4(cached_lens) || !aligned4(new_lens)))
+    return PA_ERR_INVALID_ARG;
+  if ((num_slots > 0 && (!slot_mapping || !aligned8(slot_mapping))) ||
+      (free_list_len > 0 && (!free_list || !aligned4(free_list))) ||
+      (num_groups > 0 && (!group_start || !prefix_blocks || !aligned4(group_start) ||
+                          !aligned4(prefix_blocks))))
+    return PA_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < pa_build_tables_workspace_size(num_seqs))
+    return PA_ERR_INVALID_ARG;
+  // The new lengths, the query starts and the tables are written while others
+  // of these are still read.
+  const void* written[] = {context_lens, query_start, num_free_out, block_tables};
+  const void* read[] = {new_lens, group_start, prefix_blocks, free_list, cached_lens, num_free};
+  for (const void* w : written)
+    for (const void* r : read)
+      if (w && w == r && !(w == context_lens && r == cached_lens) &&
+          !(w == num_free_out && r == num_free))
+        return PA_ERR_INVALID_ARG;
+  if ((long long)num_seqs * max_blocks_per_seq >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
+  DeviceState ds;
+  pa_status st = device_state(&ds, false);
+  if (st != PA_OK) return st;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  pa::TablesParams p{};
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.query_start = query_start;
+  p.slot_mapping = slot_mapping;
+  p.num_free_out = num_free_out;
+  p.free_list = free_list;
+  p.num_free = num_free;
+  p.cached_lens = cached_lens;
+  p.new_lens = new_lens;
+  p.group_start = group_start;
+  p.prefix_blocks = prefix_blocks;
+  p.head = reinterpret_cast<int*>(ws);
+  p.plan = reinterpret_cast<int4*>(ws + 256);
+  p.leaders = reinterpret_cast<int*>(ws + 256 + (size_t)num_seqs * sizeof(int4));
+  p.err = ds.err;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_slots = num_slots;
+  p.free_len = free_list_len;
+  p.num_groups = num_groups;
+  p.num_seqs = num_seqs;
+  p.block_size = block_size;
+  while ((1 << p.log2_block) < block_size) ++p.log2_block;
+  p.num_blocks = num_blocks;
+  return pa::launch_build_tables(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+pa_status pa_latent_write(const void* latent, int64_t latent_stride, const void* rope,
+                          int64_t rope_stride, void* cache, const int64_t* slot_mapping,
+                          int num_tokens, int latent_dim, int rope_dim, int block_size,
+                          int num_blocks, pa_stream_t stream) {
+  if (latent_dim != pa::kLatentDim || rope_dim != pa::kRopeDim || !block_size_ok(block_size))
+    return PA_ERR_UNSUPPORTED;
+  if (num_tokens < 0 || num_blocks <= 0) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (!latent || !rope || !cache || !slot_mapping || !aligned16(latent) || !aligned16(rope) ||
+      !aligned16(cache) || !aligned8(slot_mapping))
+    return PA_ERR_INVALID_ARG;
+  if (latent_stride < latent_dim || rope_stride < rope_dim || latent_stride % 8 ||
+      rope_stride % 8)
+    return PA_ERR_INVALID_ARG;
+  DeviceState ds;
+  pa_status st = device_state(&ds, false);
+  if (st != PA_OK) return st;
+  return pa::launch_latent_write(latent, latent_stride / 8, rope, rope_stride / 8, cache,
+                                 slot_mapping, num_tokens, block_size, num_blocks, ds.err,
+                                 reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+size_t pa_latent_decode_workspace_size(int num_seqs, int num_heads) {
+  if (num_seqs < 0 || num_heads <= 0 || num_heads > kMaxLatentHeads) return 0;
+  return pa::latent_workspace_bytes(num_seqs, num_heads, kWorkspaceSms);
+}
+
+pa_status pa_latent_decode(void* out, const void* query, const void* cache,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, int num_seqs, int num_heads,
+                           int latent_dim, int rope_dim, int block_size, int num_blocks,
+                           float scale, int max_context_len, void* workspace,
+                           size_t workspace_bytes, pa_stream_t stream) {
+  if (latent_dim != pa::kLatentDim || rope_dim != pa::kRopeDim || block_size < 8 ||
+      !block_size_ok(block_size))
+    return PA_ERR_UNSUPPORTED;
+  if (num_seqs < 0 || num_heads <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 ||
+      max_context_len < 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_heads > kMaxLatentHeads) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !query || !cache || !block_tables || !context_lens || !workspace)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(query) || !aligned16(cache) || !aligned16(workspace) ||
+      !aligned4(block_tables) || !aligned4(context_lens))
+    return PA_ERR_INVALID_ARG;
+  if (workspace_bytes < pa_latent_decode_workspace_size(num_seqs, num_heads))
+    return PA_ERR_INVALID_ARG;
+  // 32-bit row coordinates of the copies (one past the last row included).
+  if ((long long)num_blocks * block_size >= (1LL << 31) - 64 ||
+      (long long)num_seqs * num_heads >= (1LL << 31) - 64)
+    return PA_ERR_UNSUPPORTED;
+  DeviceState ds;
+  pa_status st = device_state(&ds, false);
+  if (st != PA_OK) return st;
+  pa::LatentArgs g{};
+  g.out = out;
+  g.query = query;
+  g.cache = cache;
+  g.block_tables = block_tables;
+  g.context_lens = context_lens;
+  g.workspace = static_cast<unsigned char*>(workspace);
+  g.err = ds.err;
+  g.num_seqs = num_seqs;
+  g.num_heads = num_heads;
+  g.block_size = block_size;
+  g.num_blocks = num_blocks;
+  g.max_blocks = max_blocks_per_seq;
+  g.max_context_len = max_context_len;
+  g.sms = ds.sms < kWorkspaceSms ? ds.sms : kWorkspaceSms;
+  g.scale_log2 = (float)((double)scale * 1.4426950408889634073599246810019);
+  return pa::launch_latent_decode(g, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }

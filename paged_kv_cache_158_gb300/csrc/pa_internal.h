@@ -131,4 +131,54 @@ cudaError_t launch_slot_mapping(int64_t* slot_mapping, const int32_t* block_tabl
                                 int block_size, int num_blocks, unsigned int* err,
                                 cudaStream_t stream);
 
+// Block tables and slot map from request lengths: arguments as in
+// pa_build_tables.
+struct TablesParams {
+  int32_t* block_tables;         // [S][max_blocks]
+  int32_t* context_lens;         // [S]
+  int32_t* query_start;          // [S + 1]
+  int64_t* slot_mapping;         // [num_slots]
+  int32_t* num_free_out;         // [1]
+  const int32_t* free_list;      // [free_len]
+  const int32_t* num_free;       // [1]
+  const int32_t* cached_lens;    // [S]
+  const int32_t* new_lens;       // [S]
+  const int32_t* group_start;    // [num_groups + 1]
+  const int32_t* prefix_blocks;  // [num_groups]
+  int* head;                     // workspace: the free count on entry
+  int4* plan;                    // workspace: [S] cached, held, off, prefix blocks
+  int* leaders;                  // workspace: [S]
+  unsigned int* err;
+  int max_blocks, num_slots, free_len, num_groups, num_seqs, block_size, log2_block, num_blocks;
+};
+// Steps of at most this many slots (and 1024 sequences) are filled by the
+// planning CTA, larger ones by a second kernel.
+constexpr int kFillInPlan = 4096;
+cudaError_t launch_build_tables(const TablesParams& p, cudaStream_t stream);
+
+// Latent cache: rows of kLatentDim latent and kRopeDim rotary values.
+constexpr int kLatentDim = 512;
+constexpr int kRopeDim = 64;
+constexpr int kLatentRow = kLatentDim + kRopeDim;
+
+// Strides in 16-byte vectors.
+cudaError_t launch_latent_write(const void* latent, long long latent_stride, const void* rope,
+                                long long rope_stride, void* cache, const int64_t* slot_mapping,
+                                int num_tokens, int block_size, int num_blocks, unsigned int* err,
+                                cudaStream_t stream);
+
+struct LatentArgs {
+  void* out;                    // fp16 [S][H][kLatentDim]
+  const void* query;            // fp16 [S][H][kLatentRow]
+  const void* cache;            // fp16 [NB][B][kLatentRow]
+  const int32_t* block_tables;  // [S][max_blocks]
+  const int32_t* context_lens;  // [S]
+  unsigned char* workspace;
+  unsigned int* err;
+  int num_seqs, num_heads, block_size, num_blocks, max_blocks, max_context_len, sms;
+  float scale_log2;
+};
+size_t latent_workspace_bytes(int num_seqs, int num_heads, int sms);
+cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream);
+
 }  // namespace pa

@@ -42,7 +42,6 @@
 //    back to back (one CTA per SM by shared memory).
 #include <cuda.h>
 #include <cuda_fp16.h>
-#include <cudaTypedefs.h>
 
 #include <mutex>
 
@@ -50,6 +49,7 @@
 #include "pa_internal.h"
 #include "pa_launch.cuh"
 #include "pa_prefill_rows.cuh"
+#include "pa_tensormap.cuh"
 #include "pa_umma.cuh"
 
 namespace pa {
@@ -741,34 +741,6 @@ __global__ void __launch_bounds__(PrefillTraits<D, F8>::THREADS, 1)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-// fp16 tensors with 128-byte swizzle (operand layout), or bytes unswizzled
-// (FP8 codes, widened in shared memory).
-bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-            const cuuint64_t* strides, const cuuint32_t* box, bool bytes = false) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-            (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE,
-            bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool F8>
 cudaError_t launch_prefill_t(const PrefillArgs& g, cudaStream_t stream) {
   using T = PrefillTraits<D, F8>;
@@ -793,9 +765,9 @@ cudaError_t launch_prefill_t(const PrefillArgs& g, cudaStream_t stream) {
   const cuuint64_t kstr[1] = {(cuuint64_t)D * (F8 ? 1 : 2)};
   // fp16: boxes of one 64-element swizzle atom; FP8: one box covers a row.
   const cuuint32_t kbox[2] = {(cuuint32_t)(F8 ? D : 64), (cuuint32_t)g.block_size};
-  if (!encode(&tq, g.query, 3, qdims, qstr, qbox) ||
-      !encode(&tk, g.key_cache, 2, kdims, kstr, kbox, F8) ||
-      !encode(&tv, g.value_cache, 2, kdims, kstr, kbox, F8))
+  if (!encode_tensor_map(&tq, g.query, 3, qdims, qstr, qbox) ||
+      !encode_tensor_map(&tk, g.key_cache, 2, kdims, kstr, kbox, F8) ||
+      !encode_tensor_map(&tv, g.value_cache, 2, kdims, kstr, kbox, F8))
     return cudaErrorInvalidValue;
   PrefillParams p{};
   p.out = g.out;

@@ -1,0 +1,334 @@
+// Block tables, context lengths, query starts and the slot map of a step,
+// built on the GPU from request lengths and a free list.
+//
+// What is computed ("深入解析LLM推理引擎：从PagedAttention到调度优化" §3.2-§3.3: a
+// sequence takes a block when its last one is full, the free list pops its
+// last entry; "vLLM推理加速深度解读：PagedAttention如何提升10x吞吐量" §2.3 address map):
+// with c = cached + new tokens of sequence s, held = ceil(cached / B) (a
+// member of a group other than its first: at least the group's prefix
+// blocks) and need = max(0, ceil(c / B) - held),
+//   off_s = sum of need over the sequences before s,
+//   table[s][held + k] = free[num_free - 1 - (off_s + k)]   for k < need,
+//   slot of the token at position p = table[s][p / B] * B + p % B.
+//
+// Design (GB300): the sums over sequences are a scan of a few thousand
+// integers, so one CTA plans the call: it keeps every length in registers or
+// re-reads it from L2, and nothing but the launch and two dependent loads
+// bounds it.  The plan (per sequence: cached, held, off, prefix blocks,
+// leader) goes to the workspace.  Filling the tables and slots is 8 bytes a
+// token and 4 a block of stores, spread over a grid by a second kernel; a
+// step whose slots one CTA stores in less time than the second kernel takes
+// to follow (kFillInPlan) is filled by the planning CTA itself, from the plan
+// in shared memory.  Context lengths and the free count are written after
+// every read of the old ones, so both may be updated in place.
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_launch.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kFillThreads = 256;
+constexpr int kFillTokens = 1024;  // tokens of one CTA of the fill kernel
+constexpr int kGroupsInSmem = 1024;
+
+struct SeqPlan {
+  int cached;  // tokens in the cache before the step
+  int held;    // blocks of the row that are set before the step
+  int off;     // blocks taken by the sequences before this one
+  int pre;     // leading entries that come from the leader's row
+};
+
+// One sequence's lengths as the call uses them.
+struct SeqLens {
+  int cached, fresh;
+  bool bad;
+};
+
+__device__ __forceinline__ SeqLens read_lens(const TablesParams& a, int s) {
+  const int cap = (int)min((long long)a.max_blocks * a.block_size, 0x7fffffffLL);
+  SeqLens r;
+  r.cached = a.cached_lens[s];
+  r.fresh = a.new_lens[s];
+  r.bad = r.cached < 0 || r.cached > cap || r.fresh < 0 || r.fresh > cap - r.cached;
+  if (r.bad) {
+    r.cached = min(max(r.cached, 0), cap);
+    r.fresh = 0;
+  }
+  return r;
+}
+
+__device__ __forceinline__ int blocks_of(int tokens, int log2_block) {
+  return (int)(((long long)tokens + (1 << log2_block) - 1) >> log2_block);
+}
+
+// The group of sequence s, or -1.  Malformed starts give no group.
+__device__ __forceinline__ int group_of(const int32_t* starts, int num_groups, int num_seqs, int s) {
+  int lo = 0, hi = num_groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (starts[mid] <= s) lo = mid; else hi = mid - 1;
+  }
+  if (num_groups <= 0) return -1;
+  const int b = starts[lo], e = starts[lo + 1];
+  return b >= 0 && b <= s && s < e && e <= num_seqs ? lo : -1;
+}
+
+// Plan of sequence s: what it takes when the call has enough blocks (fits),
+// or the state it keeps when it has not.
+__device__ __forceinline__ void plan_seq(const TablesParams& a, const int32_t* starts, int s,
+                                         bool fits, bool report, SeqPlan* p, int* leader,
+                                         int* fresh, int* need) {
+  const SeqLens x = read_lens(a, s);
+  if (report && x.bad) atomicOr(a.err, PA_ERRBIT_CONTEXT);
+  *fresh = fits ? x.fresh : 0;
+  const int own = blocks_of(x.cached, a.log2_block);
+  p->cached = x.cached;
+  p->pre = 0;
+  *leader = s;
+  if (a.num_groups > 0) {
+    const int g = group_of(starts, a.num_groups, a.num_seqs, s);
+    if (g >= 0 && starts[g] != s) {
+      *leader = starts[g];
+      const SeqLens l = read_lens(a, *leader);
+      const int want = a.prefix_blocks[g];
+      const int has = blocks_of(l.cached + (fits ? l.fresh : 0), a.log2_block);
+      p->pre = min(max(want, 0), has);
+      if (report && fits && p->pre != want) atomicOr(a.err, PA_ERRBIT_CONTEXT);
+    }
+  }
+  p->held = max(own, p->pre);
+  *need = max(0, blocks_of(x.cached + *fresh, a.log2_block) - p->held);
+}
+
+// Fills the row of sequence s: the shared entries and the new blocks.  `step`
+// threads of the warp or CTA call it with their index.
+__device__ __forceinline__ void fill_row(const TablesParams& a, const SeqPlan& p, const SeqPlan& lead,
+                                         int s, int leader, int nb, int num_free, int idx, int step) {
+  int32_t* row = a.block_tables + (size_t)s * a.max_blocks;
+  const int32_t* lrow = a.block_tables + (size_t)leader * a.max_blocks;
+  for (int j = idx; j < p.pre; j += step)
+    row[j] = j < lead.held ? lrow[j] : a.free_list[num_free - 1 - (lead.off + j - lead.held)];
+  for (int j = p.held + idx; j < nb; j += step)
+    row[j] = a.free_list[num_free - 1 - (p.off + j - p.held)];
+}
+
+// The slot of the token at position pos of sequence s; -1 in a shared block
+// of another sequence (its leader writes it) and for a bad block id.
+__device__ __forceinline__ int64_t slot_of(const TablesParams& a, const SeqPlan& p, int s, int pos,
+                                           int num_free) {
+  const int j = pos >> a.log2_block;
+  if (j < p.pre) return -1;
+  const int id = j < p.held ? a.block_tables[(size_t)s * a.max_blocks + j]
+                            : a.free_list[num_free - 1 - (p.off + j - p.held)];
+  if (id < 0 || id >= a.num_blocks) {
+    atomicOr(a.err, PA_ERRBIT_TOKEN);
+    return -1;
+  }
+  return ((int64_t)id << a.log2_block) | (pos & (a.block_size - 1));
+}
+
+// Last s in [lo, hi] with starts[s] <= t.
+__device__ __forceinline__ int last_at_most(const int* starts, int lo, int hi, int t) {
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (starts[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Inclusive sums of (x, y) over the block; the totals in *tx, *ty.  `sums`:
+// 64 values of shared memory.
+__device__ __forceinline__ void block_scan2(long long& x, long long& y, long long* sums,
+                                            long long* tx, long long* ty) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(kFullMask, x, o), v = __shfl_up_sync(kFullMask, y, o);
+    if (lane >= o) {
+      x += u;
+      y += v;
+    }
+  }
+  __syncthreads();  // the sums of an earlier call have been read
+  if (lane == 31) {
+    sums[warp] = x;
+    sums[32 + warp] = y;
+  }
+  __syncthreads();
+  long long bx = 0, by = 0, ax = 0, ay = 0;
+#pragma unroll 8
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    const long long u = sums[w], v = sums[32 + w];
+    if (w < warp) {
+      bx += u;
+      by += v;
+    }
+    ax += u;
+    ay += v;
+  }
+  x += bx;
+  y += by;
+  *tx = ax;
+  *ty = ay;
+}
+
+// FILL: up to kPlanThreads sequences and kFillInPlan slots, filled here.
+template <bool FILL>
+__global__ void __launch_bounds__(kPlanThreads) tables_plan_kernel(const TablesParams a) {
+  __shared__ long long sums[64];
+  __shared__ int32_t starts_s[kGroupsInSmem + 1];
+  __shared__ SeqPlan plan_s[FILL ? kPlanThreads : 1];
+  __shared__ int lead_s[FILL ? kPlanThreads : 1];
+  __shared__ int qs_s[FILL ? kPlanThreads + 1 : 1];
+  const int tid = threadIdx.x, S = a.num_seqs;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int nf = *a.num_free;
+  const bool nf_ok = nf >= 0 && nf <= a.free_len;
+  const int32_t* starts = a.group_start;
+  if (a.num_groups > 0 && a.num_groups <= kGroupsInSmem) {
+    for (int i = tid; i <= a.num_groups; i += kPlanThreads) starts_s[i] = a.group_start[i];
+    starts = starts_s;
+    __syncthreads();
+  }
+  SeqPlan p{};
+  int leader = 0, fresh = 0, need = 0;
+  // Totals of the call: does it fit the free list (and 32-bit token numbers)?
+  long long tb = 0, tt = 0, ib = 0, it = 0;
+  {
+    long long nb = 0, nt = 0;
+    for (int s = tid; s < S; s += kPlanThreads) {
+      plan_seq(a, starts, s, true, true, &p, &leader, &fresh, &need);
+      nb += need;
+      nt += fresh;
+    }
+    ib = nb;
+    it = nt;
+    block_scan2(ib, it, sums, &tb, &tt);
+  }
+  const bool fits = tb <= (nf_ok ? nf : 0) && tt <= 0x7fffffffLL;
+  if (tid == 0 && (!fits || !nf_ok)) atomicOr(a.err, PA_ERRBIT_POOL);
+  long long carry_b = 0, carry_t = 0;
+  for (int base = 0; base < S; base += kPlanThreads) {
+    const int s = base + tid;
+    if (S > kPlanThreads || !fits) {  // one pass: the first scan above is the answer
+      need = fresh = 0;
+      if (s < S) plan_seq(a, starts, s, fits, false, &p, &leader, &fresh, &need);
+      ib = need;
+      it = fresh;
+      block_scan2(ib, it, sums, &tb, &tt);
+    }
+    if (s < S) {
+      p.off = (int)(carry_b + ib - need);
+      const int q = (int)(carry_t + it - fresh);
+      a.query_start[s] = q;
+      if constexpr (FILL) {
+        plan_s[s] = p;
+        lead_s[s] = leader;
+        qs_s[s] = q;
+      } else {
+        a.plan[s] = make_int4(p.cached, p.held, p.off, p.pre);
+        a.leaders[s] = leader;
+      }
+    }
+    carry_b += tb;
+    carry_t += tt;
+  }
+  if (tid == 0) {
+    a.query_start[S] = (int)carry_t;
+    if constexpr (FILL) {
+      qs_s[S] = (int)carry_t;
+    } else {
+      a.head[0] = nf;
+    }
+    *a.num_free_out = fits ? nf - (int)carry_b : nf;
+    if (carry_t > a.num_slots) atomicOr(a.err, PA_ERRBIT_TOKEN);
+  }
+  __syncthreads();  // every read of cached_lens is done: context_lens may be the same array
+  if constexpr (FILL) {
+    // The sequence's length from the plan: only one round of sequences.
+    if (tid < S) a.context_lens[tid] = plan_s[tid].cached + (qs_s[tid + 1] - qs_s[tid]);
+    const int lane = tid & 31;
+    for (int s = tid >> 5; s < S; s += kPlanThreads / 32) {
+      const SeqPlan x = plan_s[s];
+      const int l = lead_s[s];
+      const int c = x.cached + (qs_s[s + 1] - qs_s[s]);
+      fill_row(a, x, plan_s[l], s, l, blocks_of(c, a.log2_block), nf, lane, 32);
+    }
+    const int total = qs_s[S];
+    for (int t = tid; t < a.num_slots; t += kPlanThreads) {
+      int64_t slot = -1;
+      if (t < total) {
+        const int s = last_at_most(qs_s, 0, S - 1, t);
+        slot = slot_of(a, plan_s[s], s, plan_s[s].cached + (t - qs_s[s]), nf);
+      }
+      a.slot_mapping[t] = slot;
+    }
+  } else {
+    for (int s = tid; s < S; s += kPlanThreads) {
+      const SeqLens x = read_lens(a, s);
+      a.context_lens[s] = x.cached + (fits ? x.fresh : 0);
+    }
+  }
+}
+
+// Fills slots and rows from the plan in the workspace.  CTAs [0, slot_ctas)
+// take kFillTokens slots each; the rest take the rows, a warp a sequence.
+__global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TablesParams a, int slot_ctas) {
+  __shared__ int range[2];
+  const int tid = threadIdx.x, S = a.num_seqs;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int nf = a.head[0];
+  auto plan = [&](int s) {
+    const int4 v = a.plan[s];
+    SeqPlan p;
+    p.cached = v.x;
+    p.held = v.y;
+    p.off = v.z;
+    p.pre = v.w;
+    return p;
+  };
+  const int total = a.query_start[S];
+  if ((int)blockIdx.x < slot_ctas) {
+    const int t0 = (int)blockIdx.x * kFillTokens;
+    const int t1 = min(t0 + kFillTokens, a.num_slots) - 1;
+    // The sequences of the CTA's first and last token bound every search.
+    if (tid < 2) range[tid] = last_at_most(a.query_start, 0, S - 1, tid == 0 ? t0 : t1);
+    __syncthreads();
+    const int lo = range[0], hi = range[1];
+    for (int t = t0 + tid; t <= t1; t += kFillThreads) {
+      int64_t slot = -1;
+      if (t < total) {
+        const int s = last_at_most(a.query_start, lo, hi, t);
+        const SeqPlan p = plan(s);
+        slot = slot_of(a, p, s, p.cached + (t - a.query_start[s]), nf);
+      }
+      a.slot_mapping[t] = slot;
+    }
+    return;
+  }
+  const int s = ((int)blockIdx.x - slot_ctas) * (kFillThreads / 32) + (tid >> 5);
+  if (s >= S) return;
+  const SeqPlan p = plan(s);
+  const int l = a.leaders[s];
+  const int c = p.cached + (a.query_start[s + 1] - a.query_start[s]);
+  fill_row(a, p, plan(l), s, l, blocks_of(c, a.log2_block), nf, tid & 31, 32);
+}
+
+}  // namespace
+
+cudaError_t launch_build_tables(const TablesParams& p, cudaStream_t stream) {
+  if (p.num_seqs <= kPlanThreads && p.num_slots <= kFillInPlan)
+    return launch_pdl(tables_plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, stream, p);
+  cudaError_t e = launch_pdl(tables_plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, stream, p);
+  if (e != cudaSuccess) return e;
+  const int slot_ctas = (int)(((long long)p.num_slots + kFillTokens - 1) / kFillTokens);
+  const int row_ctas = (p.num_seqs + kFillThreads / 32 - 1) / (kFillThreads / 32);
+  return launch_pdl(tables_fill_kernel, dim3(slot_ctas + row_ctas), dim3(kFillThreads), 0, stream, p,
+                    slot_ctas);
+}
+
+}  // namespace pa
