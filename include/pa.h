@@ -178,6 +178,71 @@ pa_status pa_decode_append(void* out, const void* query, const void* key_new,
                            void* workspace, size_t workspace_bytes, unsigned int flags,
                            pa_stream_t stream);
 
+/*
+ * Decode attention of a batch whose groups of sequences share a prefix: the
+ * result of pa_decode, with a group's shared blocks read and attended to once
+ * for all its sequences (on the tensor cores) instead of once for each
+ * [P3 §2.3: sequences with a common prefix have the same blocks in their
+ * tables; P2 §2.1, §2.3: the attention].  The sequences
+ * [group_start[g], group_start[g+1]) form group g, and the first
+ * prefix_blocks[g] entries of their block tables are the same blocks.  Each
+ * sequence's remaining tokens are attended to by the decode's own pass, and
+ * the parts are joined by their log-sum-exp.
+ *
+ *   out, query, key_cache, value_cache, block_tables, context_lens, scale,
+ *   max_context_len      as for pa_decode, and the same errors
+ *   group_start    int32 [num_groups + 1], not decreasing, within
+ *                  [0, num_seqs]; sequences outside every group share nothing
+ *   prefix_blocks  int32 [num_groups]: whole blocks shared, >= 0
+ *                  (both may be NULL when num_groups == 0)
+ *   max_prefix_len host-side bound of the shared tokens used: a longer prefix
+ *                  is shared up to it (whole blocks) and the rest read for
+ *                  each sequence; the result is the same attention
+ *   workspace      pa_decode_shared_workspace_size(...) bytes, 16-byte
+ *                  aligned; contents ignored.  Calls that share one must not
+ *                  overlap on the GPU.
+ *
+ * That the entries are equal is the caller's word: the table row of one member
+ * is read for the whole group.  A member whose context is shorter than the
+ * prefix is computed by itself from its own row, and so are the members of a
+ * group in which fewer than two cover it, and prefixes in blocks of 4
+ * tokens.  Bounds that decrease or leave [0, num_seqs], or a negative
+ * prefix_blocks, set PA_ERRBIT_CONTEXT and nothing is shared.
+ *
+ * Arithmetic: the suffix as pa_decode; the prefix as pa_prefill (fp16 products
+ * with fp32 accumulation, softmax in fp32 with the weights rounded once to
+ * fp16, the sum adding the rounded weights); partial results in fp32, the
+ * result rounded once to fp16.  The prefix is split among SMs by the whole
+ * batch, so the last bits may depend on the other groups; the same call gives
+ * the same bits.
+ * num_groups <= num_seqs; num_blocks * num_heads * block_size < 2^31 - 1.
+ */
+size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int num_heads, int head_dim,
+                                       int max_context_len, int max_prefix_len);
+pa_status pa_decode_shared(void* out, const void* query, const void* key_cache,
+                           const void* value_cache, const int32_t* block_tables,
+                           int max_blocks_per_seq, const int32_t* context_lens,
+                           const int32_t* group_start, const int32_t* prefix_blocks,
+                           int num_groups, int num_seqs, int num_heads, int head_dim,
+                           int block_size, int num_blocks, float scale, int max_context_len,
+                           int max_prefix_len, void* workspace, size_t workspace_bytes,
+                           pa_stream_t stream);
+
+/*
+ * pa_decode_shared over FP8 (E4M3) caches (format and scaling as for
+ * pa_decode_fp8): the codes are widened to fp16 exactly, the key scale is
+ * folded into the logit scale and the value scale applied to the partial
+ * outputs.  k_scale and v_scale must be finite and positive.
+ */
+pa_status pa_decode_shared_fp8(void* out, const void* query, const void* key_cache,
+                               const void* value_cache, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* context_lens,
+                               const int32_t* group_start, const int32_t* prefix_blocks,
+                               int num_groups, int num_seqs, int num_heads, int head_dim,
+                               int block_size, int num_blocks, float scale, float k_scale,
+                               float v_scale, int max_context_len, int max_prefix_len,
+                               void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
 /* Size of the fixed scratch area pa_decode_noalloc uses (32 MiB per device). */
 #define PA_DECODE_NOALLOC_SCRATCH_BYTES (32u * 1024u * 1024u)
 

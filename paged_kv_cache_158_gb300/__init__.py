@@ -99,6 +99,14 @@ _lib.pa_latent_decode_workspace_size.restype = _sz
 _lib.pa_latent_decode.argtypes = [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32,
                                   _i32, _vp, _sz, _vp]
 _lib.pa_latent_decode.restype = _i32
+_lib.pa_decode_shared_workspace_size.argtypes = [_i32] * 6
+_lib.pa_decode_shared_workspace_size.restype = _sz
+_lib.pa_decode_shared.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                                  _i32, _i32, _f32, _i32, _i32, _vp, _sz, _vp]
+_lib.pa_decode_shared.restype = _i32
+_lib.pa_decode_shared_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32,
+                                      _i32, _i32, _i32, _f32, _f32, _f32, _i32, _i32, _vp, _sz, _vp]
+_lib.pa_decode_shared_fp8.restype = _i32
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_OUT_OF_RANGE, PA_ERR_TIMEOUT = range(6)
 PA_ERRBIT_BLOCK_ID, PA_ERRBIT_CONTEXT, PA_ERRBIT_SLOT = 0x1, 0x2, 0x4
@@ -511,6 +519,66 @@ def _same_device(*tensors) -> None:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
 
 
+def pa_decode_shared_workspace_size(num_seqs: int, num_groups: int, num_heads: int, head_dim: int,
+                                    max_context_len: int, max_prefix_len: int) -> int:
+    return int(_lib.pa_decode_shared_workspace_size(num_seqs, num_groups, num_heads, head_dim,
+                                                    max_context_len, max_prefix_len))
+
+
+def decode_shared_workspace(num_seqs: int, num_groups: int, num_heads: int, head_dim: int,
+                            max_context_len: int, max_prefix_len: int, device=None) -> torch.Tensor:
+    """A device byte buffer of pa_decode_shared_workspace_size(...) bytes."""
+    n = pa_decode_shared_workspace_size(num_seqs, num_groups, num_heads, head_dim, max_context_len,
+                                        max_prefix_len)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_decode_shared(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                     value_cache: torch.Tensor, block_tables: torch.Tensor,
+                     context_lens: torch.Tensor, group_start: torch.Tensor,
+                     prefix_blocks: torch.Tensor, scale: float, max_context_len: int,
+                     max_prefix_len: int, workspace: torch.Tensor, stream=None) -> None:
+    """pa_decode for a batch whose sequences [group_start[g], group_start[g+1]) share their first
+    prefix_blocks[g] blocks, each group's prefix attended to once (see pa_decode_shared in
+    include/pa.h)."""
+    _decode_shared(out, query, key_cache, value_cache, block_tables, context_lens, group_start,
+                   prefix_blocks, scale, None, max_context_len, max_prefix_len, workspace, stream)
+
+
+def pa_decode_shared_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                         value_cache: torch.Tensor, block_tables: torch.Tensor,
+                         context_lens: torch.Tensor, group_start: torch.Tensor,
+                         prefix_blocks: torch.Tensor, scale: float, k_scale: float, v_scale: float,
+                         max_context_len: int, max_prefix_len: int, workspace: torch.Tensor,
+                         stream=None) -> None:
+    """pa_decode_shared over FP8 (E4M3, uint8) caches with per-tensor scales."""
+    _decode_shared(out, query, key_cache, value_cache, block_tables, context_lens, group_start,
+                   prefix_blocks, scale, (float(k_scale), float(v_scale)), max_context_len,
+                   max_prefix_len, workspace, stream)
+
+
+def _decode_shared(out, query, key_cache, value_cache, block_tables, context_lens, group_start,
+                   prefix_blocks, scale, fp8, max_context_len, max_prefix_len, workspace, stream) -> None:
+    S, H, D, B, NB = _decode_shapes(out, query, key_cache, value_cache, block_tables, context_lens)
+    G = prefix_blocks.shape[0]
+    if group_start.shape != (G + 1,) or prefix_blocks.dim() != 1:
+        raise ValueError("group_start must be [num_groups + 1] and prefix_blocks [num_groups]")
+    _same_device(out, query, key_cache, value_cache, block_tables, context_lens, group_start,
+                 prefix_blocks, workspace)
+    name = "pa_decode_shared" if fp8 is None else "pa_decode_shared_fp8"
+    st = getattr(_lib, name)(_ptr(out, "out", torch.float16), _ptr(query, "query", torch.float16),
+                             _cache_ptr(key_cache, "key_cache", fp8 is not None),
+                             _cache_ptr(value_cache, "value_cache", fp8 is not None),
+                             _ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+                             _ptr(context_lens, "context_lens", torch.int32),
+                             _ptr(group_start, "group_start", torch.int32),
+                             _ptr(prefix_blocks, "prefix_blocks", torch.int32), G, S, H, D, B, NB,
+                             float(scale), *(fp8 or ()), int(max_context_len), int(max_prefix_len),
+                             _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
+                             _stream(stream))
+    _check(st, name)
+
+
 def pa_build_tables_workspace_size(num_seqs: int) -> int:
     return int(_lib.pa_build_tables_workspace_size(num_seqs))
 
@@ -654,6 +722,7 @@ __all__ = [
     "pa_swap_blocks", "pa_prefill", "pa_prefill_fp8", "pa_decode_noalloc", "pa_decode_ex",
     "pa_decode_fp8_ex", "pa_decode_append", "pa_decode_append_fp8", "pa_prefill_ex",
     "pa_prefill_fp8_ex", "pa_build_tables", "pa_build_tables_workspace_size", "build_tables_workspace",
+    "pa_decode_shared", "pa_decode_shared_fp8", "pa_decode_shared_workspace_size", "decode_shared_workspace",
     "pa_latent_write", "pa_latent_decode", "pa_latent_decode_workspace_size", "latent_decode_workspace",
     "pa_status_string", "pa_decode_workspace_size", "pa_decode_partition_tokens",
     "pa_decode_set_partition_tokens", "decode_workspace", "raise_on_device_errors", "PAError",

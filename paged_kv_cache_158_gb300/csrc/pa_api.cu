@@ -12,7 +12,7 @@ namespace pa {
 #define PA_DECLARE_DECODE(sfx)                                                           \
   cudaError_t launch_decode_partition_##sfx(const DecodeParams&, int, int, size_t,      \
                                             cudaStream_t);                              \
-  int decode_ctas_per_sm_##sfx(int, size_t, bool);                                      \
+  int decode_ctas_per_sm_##sfx(int, size_t, bool, bool);                                \
   size_t decode_fixed_smem_##sfx(int);                                                  \
   cudaError_t decode_prepare_##sfx();
 PA_DECLARE_DECODE(d64)
@@ -39,22 +39,23 @@ cudaError_t launch_decode_reduce(const DecodeParams& p, int head_dim, int block_
 }
 
 size_t decode_smem_bytes(bool fp8, int head_dim, int block_size, int part_tokens,
-                         int seqs_in_launch) {
+                         int seqs_in_launch, bool shared) {
   const size_t fixed =
       fp8 ? (head_dim == 64 ? decode_fixed_smem_f8_d64(block_size)
                             : decode_fixed_smem_f8_d128(block_size))
           : (head_dim == 64 ? decode_fixed_smem_d64(block_size) : decode_fixed_smem_d128(block_size));
   const size_t bt = 2 * (size_t)(part_tokens / block_size + 1) * 4;
-  const size_t seq = (2 * (size_t)seqs_in_launch + 1) * 4 + (size_t)seqs_in_launch;  // + clip flags
+  // Cumulated items, lengths, and the clip flags or (shared) the first positions.
+  const size_t seq = (2 * (size_t)seqs_in_launch + 1) * 4 + (size_t)seqs_in_launch * (shared ? 4 : 1);
   return (fixed + bt + seq + 15) & ~size_t(15);
 }
 
-int decode_ctas_per_sm(bool fp8, int head_dim, int block_size, size_t smem, bool append) {
+int decode_ctas_per_sm(bool fp8, int head_dim, int block_size, size_t smem, bool append, bool shared) {
   if (fp8)
-    return head_dim == 64 ? decode_ctas_per_sm_f8_d64(block_size, smem, append)
-                          : decode_ctas_per_sm_f8_d128(block_size, smem, append);
-  return head_dim == 64 ? decode_ctas_per_sm_d64(block_size, smem, append)
-                        : decode_ctas_per_sm_d128(block_size, smem, append);
+    return head_dim == 64 ? decode_ctas_per_sm_f8_d64(block_size, smem, append, shared)
+                          : decode_ctas_per_sm_f8_d128(block_size, smem, append, shared);
+  return head_dim == 64 ? decode_ctas_per_sm_d64(block_size, smem, append, shared)
+                        : decode_ctas_per_sm_d128(block_size, smem, append, shared);
 }
 
 cudaError_t decode_prepare_device(int) {
@@ -195,7 +196,8 @@ struct WsLayout {
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
-WsLayout ws_layout(int S, int H, int D, int max_context_len) {
+// partials: room for them even where no sequence has two partitions.
+WsLayout ws_layout(int S, int H, int D, int max_context_len, bool partials = false) {
   WsLayout w{};
   w.part_tokens = part_tokens_for(S, H, max_context_len);
   w.max_parts = max_context_len > 0 ? (max_context_len + w.part_tokens - 1) / w.part_tokens : 1;
@@ -209,7 +211,7 @@ WsLayout ws_layout(int S, int H, int D, int max_context_len) {
   off = round256(off);
   w.ml_off = off;
   w.o_off = off;
-  if (w.max_parts > 1) {
+  if (w.max_parts > 1 || partials) {
     const size_t slots = (size_t)S * H * w.max_parts;
     w.o_off = round256(off + slots * 2 * 4);
     off = round256(w.o_off + slots * (size_t)D * 4);
@@ -302,6 +304,94 @@ pa_status decode_impl(bool fp8, void* out, const void* query, const void* key_ca
       return PA_ERR_CUDA;
   }
   return PA_OK;
+}
+
+// Decode behind shared prefixes, for both cache element types.
+pa_status decode_shared_impl(bool fp8, void* out, const void* query, const void* key_cache,
+                             const void* value_cache, const int32_t* block_tables,
+                             int max_blocks_per_seq, const int32_t* context_lens,
+                             const int32_t* group_start, const int32_t* prefix_blocks,
+                             int num_groups, int num_seqs, int num_heads, int head_dim,
+                             int block_size, int num_blocks, float scale, float k_scale,
+                             float v_scale, int max_context_len, int max_prefix_len,
+                             void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return PA_ERR_INVALID_ARG;
+  if (num_seqs < 0 || num_groups < 0 || num_heads <= 0 || num_blocks <= 0 ||
+      max_blocks_per_seq <= 0 || max_context_len < 0 || max_prefix_len < 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !query || !key_cache || !value_cache || !block_tables || !context_lens || !workspace ||
+      (num_groups > 0 && (!group_start || !prefix_blocks)))
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache) ||
+      !aligned16(workspace) || !aligned4(block_tables) || !aligned4(context_lens) ||
+      !aligned4(group_start) || !aligned4(prefix_blocks))
+    return PA_ERR_INVALID_ARG;
+  if (num_groups > num_seqs) return PA_ERR_INVALID_ARG;
+  const WsLayout w = ws_layout(num_seqs, num_heads, head_dim, max_context_len, true);
+  const size_t pre = pa::shared_workspace_bytes(num_seqs, num_groups, num_heads, head_dim, kWorkspaceSms);
+  if (workspace_bytes < round256(w.total) + pre) return PA_ERR_INVALID_ARG;
+  // 32-bit item, tile and row numbers.
+  const long long units = ((long long)num_seqs / 128 + num_groups) * num_heads;
+  if ((long long)num_seqs * num_heads * w.max_parts >= (1LL << 31) ||
+      units * (max_prefix_len / 128 + 1) >= (1LL << 31) ||
+      !pa::prefill_rows_fit(num_blocks, num_heads, block_size))
+    return PA_ERR_UNSUPPORTED;
+  DeviceState ds;
+  pa_status st = device_state(&ds, true);
+  if (st != PA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  pa::SharedArgs g{};
+  pa::DecodeParams& p = g.dec;
+  p.out = out;
+  p.query = query;
+  p.key_cache = key_cache;
+  p.value_cache = value_cache;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.ws_ml = reinterpret_cast<float*>(ws + w.ml_off);
+  p.ws_o = reinterpret_cast<float*>(ws + w.o_off);
+  p.counter = reinterpret_cast<unsigned int*>(ws + w.counters_off);
+  p.err = ds.err;
+  p.num_heads = num_heads;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.max_context_len = max_context_len;
+  p.part_tokens = w.part_tokens;
+  p.max_parts = w.max_parts;
+  p.scale_log2 = (float)((double)scale * (double)k_scale * 1.4426950408889634073599246810019);
+  p.v_scale = v_scale;
+  p.k_scale = k_scale;
+  g.group_start = group_start;
+  g.prefix_blocks = prefix_blocks;
+  g.workspace = ws + round256(w.total);
+  g.num_groups = num_groups;
+  g.num_seqs = num_seqs;
+  g.head_dim = head_dim;
+  g.block_size = block_size;
+  g.max_prefix_len = max_prefix_len;
+  g.sms = ds.sms < kWorkspaceSms ? ds.sms : kWorkspaceSms;
+  g.num_counters = w.launches;
+  g.fp8 = fp8;
+  if (pa::launch_shared_prefix(g, cs) != cudaSuccess) return PA_ERR_CUDA;
+  for (int b = 0; b < w.launches; ++b) {
+    pa::DecodeParams q = p;
+    q.seq_begin = b * pa::kMaxSeqsPerLaunch;
+    q.num_seqs = num_seqs - q.seq_begin < pa::kMaxSeqsPerLaunch ? num_seqs - q.seq_begin
+                                                                : pa::kMaxSeqsPerLaunch;
+    q.counter = p.counter + b;
+    q.inputs_ready = 0;  // the plan of this call is an input
+    const size_t smem = pa::decode_smem_bytes(fp8, head_dim, block_size, w.part_tokens, q.num_seqs, true);
+    const int per_sm = pa::decode_ctas_per_sm(fp8, head_dim, block_size, smem, false, true);
+    long long grid = (long long)per_sm * ds.sms;
+    const long long items_ub = (long long)q.num_seqs * num_heads * w.max_parts;
+    if (grid > items_ub) grid = items_ub;
+    if (pa::launch_decode_partition(q, fp8, head_dim, block_size, (int)grid, smem, cs) != cudaSuccess)
+      return PA_ERR_CUDA;
+  }
+  return pa::launch_shared_merge(g, cs) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status copy_blocks_impl(int elem_bytes, void* const* key_caches, void* const* value_caches,
@@ -677,6 +767,45 @@ pa_status pa_slot_mapping(int64_t* slot_mapping, const int32_t* block_tables,
                                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
+}
+
+size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int num_heads, int head_dim,
+                                       int max_context_len, int max_prefix_len) {
+  if (num_seqs < 0 || num_groups < 0 || num_heads <= 0 || !head_dim_ok(head_dim) ||
+      max_context_len < 0 || max_prefix_len < 0)
+    return 0;
+  return round256(ws_layout(num_seqs, num_heads, head_dim, max_context_len, true).total) +
+         pa::shared_workspace_bytes(num_seqs, num_groups, num_heads, head_dim, kWorkspaceSms);
+}
+
+pa_status pa_decode_shared(void* out, const void* query, const void* key_cache,
+                           const void* value_cache, const int32_t* block_tables,
+                           int max_blocks_per_seq, const int32_t* context_lens,
+                           const int32_t* group_start, const int32_t* prefix_blocks,
+                           int num_groups, int num_seqs, int num_heads, int head_dim,
+                           int block_size, int num_blocks, float scale, int max_context_len,
+                           int max_prefix_len, void* workspace, size_t workspace_bytes,
+                           pa_stream_t stream) {
+  return decode_shared_impl(false, out, query, key_cache, value_cache, block_tables,
+                            max_blocks_per_seq, context_lens, group_start, prefix_blocks,
+                            num_groups, num_seqs, num_heads, head_dim, block_size, num_blocks,
+                            scale, 1.f, 1.f, max_context_len, max_prefix_len, workspace,
+                            workspace_bytes, stream);
+}
+
+pa_status pa_decode_shared_fp8(void* out, const void* query, const void* key_cache,
+                               const void* value_cache, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* context_lens,
+                               const int32_t* group_start, const int32_t* prefix_blocks,
+                               int num_groups, int num_seqs, int num_heads, int head_dim,
+                               int block_size, int num_blocks, float scale, float k_scale,
+                               float v_scale, int max_context_len, int max_prefix_len,
+                               void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  return decode_shared_impl(true, out, query, key_cache, value_cache, block_tables,
+                            max_blocks_per_seq, context_lens, group_start, prefix_blocks,
+                            num_groups, num_seqs, num_heads, head_dim, block_size, num_blocks,
+                            scale, k_scale, v_scale, max_context_len, max_prefix_len, workspace,
+                            workspace_bytes, stream);
 }
 
 size_t pa_build_tables_workspace_size(int num_seqs) {

@@ -135,6 +135,12 @@ __device__ __forceinline__ int num_parts(int c, int part_tokens) {
   return c > 0 ? (c + part_tokens - 1) / part_tokens : 1;  // an empty sequence is one item
 }
 
+// Decode behind a shared prefix: partitions of the tokens [start, c), none
+// when there are none.
+__device__ __forceinline__ int num_suffix_parts(int c, int start, int part_tokens) {
+  return c > start ? (c - start + part_tokens - 1) / part_tokens : 0;
+}
+
 struct ItemInfo {
   int s;        // sequence within the launch
   int h;
@@ -146,9 +152,10 @@ struct ItemInfo {
   int nblk;     // logical blocks it touches
 };
 
-template <int B>
+template <int B, bool SHARED>
 __device__ __forceinline__ ItemInfo locate_item(int item, const int* cum, const int* ctx_s,
-                                                int nseq, int H, int part_tokens) {
+                                                const int* start_s, int nseq, int H,
+                                                int part_tokens) {
   int lo = 0, hi = nseq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -157,11 +164,11 @@ __device__ __forceinline__ ItemInfo locate_item(int item, const int* cum, const 
   ItemInfo it;
   it.s = lo;
   it.c = ctx_s[lo];
-  it.n_parts = num_parts(it.c, part_tokens);
+  it.n_parts = num_parts(it.c, part_tokens);  // SHARED: not used, every item is a partial
   const int within = item - cum[lo];
   it.p = within / H;  // head-innermost: concurrent CTAs read the same physical blocks
   it.h = within - it.p * H;
-  it.t_begin = it.p * part_tokens;
+  it.t_begin = (SHARED ? start_s[lo] : 0) + it.p * part_tokens;
   it.t_end = min(it.c, it.t_begin + part_tokens);
   it.blk0 = it.t_begin / B;
   it.nblk = it.t_end > it.t_begin ? (it.t_end - 1) / B - it.blk0 + 1 : 0;
@@ -416,7 +423,10 @@ __device__ __forceinline__ void process_chunk(const unsigned char* Ks, const uns
 
 // APPEND: the variant with the new token's cache write fused in (a separate
 // instantiation, so the plain decode keeps its registers and schedule).
-template <int D, int B, bool F8, bool APPEND>
+// SHARED: the variant behind a shared prefix: sequence s is decoded from
+// position seq_start[s] (a block boundary) on and every item is written as a
+// partial, for the merge with the prefix's.
+template <int D, int B, bool F8, bool APPEND, bool SHARED = false>
 __global__ void __launch_bounds__(DecodeTraits<D, B, F8>::THREADS, F8 ? 5 : 1)
     decode_partition_kernel(const DecodeParams a) {
   using T = DecodeTraits<D, B, F8>;
@@ -440,6 +450,7 @@ __global__ void __launch_bounds__(DecodeTraits<D, B, F8>::THREADS, F8 ? 5 : 1)
   int* ctx_s = cum + (a.num_seqs + 1);          // nseq
   // nseq flags: the sequence's context length was clipped (APPEND: no write)
   unsigned char* clip_s = reinterpret_cast<unsigned char*>(ctx_s + a.num_seqs);
+  int* start_s = ctx_s + a.num_seqs;            // SHARED: nseq first positions (no flags then)
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -480,7 +491,13 @@ __global__ void __launch_bounds__(DecodeTraits<D, B, F8>::THREADS, F8 ? 5 : 1)
         const int c = effective_len(raw, a, B, blockIdx.x == 0);
         ctx_s[i] = c;
         if constexpr (APPEND) clip_s[i] = raw != c;
-        v = H * num_parts(c, P);
+        if constexpr (SHARED) {
+          const int start = a.seq_start[a.seq_begin + i];
+          start_s[i] = start;
+          v = H * num_suffix_parts(c, start, P);
+        } else {
+          v = H * num_parts(c, P);
+        }
       }
       vals[j] = v;
       local += v;
@@ -513,7 +530,7 @@ __global__ void __launch_bounds__(DecodeTraits<D, B, F8>::THREADS, F8 ? 5 : 1)
   if (cur >= total) return;
 
   // First item's block-table slice (synchronous).
-  ItemInfo it = locate_item<B>(cur, cum, ctx_s, nseq, H, P);
+  ItemInfo it = locate_item<B, SHARED>(cur, cum, ctx_s, start_s, nseq, H, P);
   {
     const int32_t* row = a.block_tables + (size_t)(a.seq_begin + it.s) * a.max_blocks;
     for (int i = tid; i < it.nblk; i += T::THREADS) bt_s[i] = row[it.blk0 + i];
@@ -587,7 +604,7 @@ __global__ void __launch_bounds__(DecodeTraits<D, B, F8>::THREADS, F8 ? 5 : 1)
     ItemInfo nx;
     nx.t_begin = nx.t_end = 0;
     if (has_next) {
-      nx = locate_item<B>(nxt, cum, ctx_s, nseq, H, P);
+      nx = locate_item<B, SHARED>(nxt, cum, ctx_s, start_s, nseq, H, P);
       const int32_t* row = a.block_tables + (size_t)(a.seq_begin + nx.s) * a.max_blocks;
       int* dst = bt_s + (buf ^ 1) * bt_cap;
       for (int i = tid; i < nx.nblk; i += T::THREADS) cp_async_4(dst + i, row + nx.blk0 + i);
@@ -773,7 +790,7 @@ __global__ void __launch_bounds__(DecodeTraits<D, B, F8>::THREADS, F8 ? 5 : 1)
         O = fmaf(sc, mb[w * T::MS + d], O);
       }
       if constexpr (F8) O *= a.v_scale;
-      if (it.n_parts == 1) {
+      if (!SHARED && it.n_parts == 1) {
         const float r = (it.c > 0 && L > 0.f) ? O / L : 0.f;
         static_cast<__half*>(a.out)[sh * D + d] = __float2half_rn(r);
       } else {
@@ -892,6 +909,9 @@ cudaError_t launch_reduce_t(const DecodeParams& p, int total_seqs, cudaStream_t 
 
 template <int D, int B, bool F8>
 cudaError_t launch_partition_t(const DecodeParams& p, int grid, size_t smem, cudaStream_t st) {
+  if (p.seq_start != nullptr)
+    return launch_pdl(decode_partition_kernel<D, B, F8, false, true>, dim3(grid),
+                      dim3(DecodeTraits<D, B, F8>::THREADS), smem, st, p);
   if (p.key_new != nullptr)
     return launch_pdl(decode_partition_kernel<D, B, F8, true>, dim3(grid),
                       dim3(DecodeTraits<D, B, F8>::THREADS), smem, st, p);
@@ -900,10 +920,13 @@ cudaError_t launch_partition_t(const DecodeParams& p, int grid, size_t smem, cud
 }
 
 template <int D, int B, bool F8>
-int ctas_per_sm_t(size_t smem, bool append) {
+int ctas_per_sm_t(size_t smem, bool append, bool shared) {
   int n = 0;
   const cudaError_t e =
-      append ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+      shared ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                   &n, decode_partition_kernel<D, B, F8, false, true>, DecodeTraits<D, B, F8>::THREADS,
+                   smem)
+      : append ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(
                    &n, decode_partition_kernel<D, B, F8, true>, DecodeTraits<D, B, F8>::THREADS, smem)
              : cudaOccupancyMaxActiveBlocksPerMultiprocessor(
                    &n, decode_partition_kernel<D, B, F8, false>, DecodeTraits<D, B, F8>::THREADS,
@@ -917,6 +940,9 @@ cudaError_t prepare_t() {
   const cudaError_t e = cudaFuncSetAttribute(decode_partition_kernel<D, B, F8, false>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
+  const cudaError_t e2 = cudaFuncSetAttribute(decode_partition_kernel<D, B, F8, false, true>,
+                                              cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e2 != cudaSuccess) return e2;
   return cudaFuncSetAttribute(decode_partition_kernel<D, B, F8, true>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
 }

@@ -49,6 +49,9 @@ struct DecodeParams {
   // stream's earlier work, so the inputs are complete when this launch starts
   // and its prologue reads them before its own wait; 0: it waits first.
   int inputs_ready;
+  // Decode behind a shared prefix (null otherwise): [S] first position of
+  // each sequence's own part, a multiple of the block size.
+  const int32_t* seq_start;
 };
 
 // Partition-kernel launch: picks the instantiation for (cache element type,
@@ -60,10 +63,12 @@ cudaError_t launch_decode_reduce(const DecodeParams& p, int head_dim, int block_
                                  int total_seqs, cudaStream_t stream);
 // Dynamic shared memory of the partition kernel.
 size_t decode_smem_bytes(bool fp8, int head_dim, int block_size, int part_tokens,
-                         int seqs_in_launch);
+                         int seqs_in_launch, bool shared = false);
 // Resident CTAs per SM of the partition kernel (append: the variant with the
-// cache write fused in) for that shared-memory size.
-int decode_ctas_per_sm(bool fp8, int head_dim, int block_size, size_t smem_bytes, bool append);
+// cache write fused in; shared: the one behind a shared prefix) for that
+// shared-memory size.
+int decode_ctas_per_sm(bool fp8, int head_dim, int block_size, size_t smem_bytes, bool append,
+                       bool shared = false);
 // One-time per-device kernel attributes (dynamic shared memory opt-in).
 cudaError_t decode_prepare_device(int device);
 
@@ -180,5 +185,22 @@ struct LatentArgs {
 };
 size_t latent_workspace_bytes(int num_seqs, int num_heads, int sms);
 cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream);
+
+// Decode of a batch whose groups of sequences share a prefix: arguments as in
+// pa_decode_shared, and the suffix pass's partials.
+struct SharedArgs {
+  DecodeParams dec;             // the suffix pass: partials, counters, sizes
+  const int32_t* group_start;   // [num_groups + 1]
+  const int32_t* prefix_blocks; // [num_groups]
+  unsigned char* workspace;     // shared_workspace_bytes of it
+  int num_groups, num_seqs, head_dim, block_size, max_prefix_len, sms, num_counters;
+  bool fp8;
+};
+size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_heads, int head_dim, int sms);
+// The plan (it also zeroes the counters and sets dec.seq_start's array), then
+// the prefix pass.
+cudaError_t launch_shared_prefix(SharedArgs& g, cudaStream_t stream);
+// Joins prefix and suffix partials into the output.
+cudaError_t launch_shared_merge(const SharedArgs& g, cudaStream_t stream);
 
 }  // namespace pa

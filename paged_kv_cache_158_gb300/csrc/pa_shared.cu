@@ -1,0 +1,800 @@
+// Decode attention of a batch whose groups of sequences share a prefix: the
+// prefix of a group is attended to once for all its queries, on the sm_103a
+// tensor cores; every sequence's own part by the decode kernel; the two are
+// joined by their log-sum-exp.
+//
+// What is computed ("vLLM推理加速深度解读：PagedAttention如何提升10x吞吐量" §2.1 and §2.3,
+// "vLLM基础架构：核心组件、PagedAttention原理、KV Cache管理与连续批处理机制" §2.3: sequences
+// that share a prefix have the same leading blocks in their tables): the
+// decode formula, with the sum over positions split at the end P of the shared
+// blocks.  For the two parts' maxima m_a, sums l_a and unnormalised outputs o_a,
+//   out = sum_a 2^(m_a - M) o_a / sum_a 2^(m_a - M) l_a,   M = max m_a.
+//
+// Bound: HBM, the distinct K/V bytes.  A 128-token tile of K and V is 64 KB
+// (D = 128, fp16; 1.5 us of one SM's share of the bandwidth) and feeds two
+// products of up to 128 query rows (0.7 us) and their softmax (0.6 us), which
+// run beside the copies.
+//
+// Design (GB300):
+//  * Plan (one CTA): for each group the members whose context covers the
+//    prefix; the others, and groups with fewer than two such members, keep
+//    their whole context in the suffix pass.  Each sequence's first own
+//    position, each group's tiles and their running sum go to the workspace.
+//  * Prefix (one persistent CTA per SM): units are (group, 128 members, head);
+//    the tiles of all units are numbered in that order and cut into equal
+//    ranges, so few groups with long prefixes load every SM alike.  A worker's
+//    part of a unit is one segment; its rows go to partial rows
+//    H * s0 + h * rows + 128 * w (s0: the unit's first sequence; w: the
+//    worker), distinct because along the walk either the unit or w grows.
+//  * Warps: four softmax warps (one query row a thread), TMA, MMA, and for
+//    E4M3 caches four that widen the codes to fp16 in shared memory (exact).
+//    The K/V rings are as deep as the shared memory allows, S is
+//    double-buffered in tensor memory, P (fp16, rounded once) lies over the
+//    first half of its S, and the products of S(t + 1) and P.V(t) are issued
+//    in the order in which they become ready.
+//  * Suffix: the decode's partition kernel from each sequence's first own
+//    position on.  Merge: a warp per (sequence, head).
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_launch.cuh"
+#include "pa_tensormap.cuh"
+#include "pa_umma.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kRows = 128;    // query rows of a unit (MMA M)
+constexpr int kTile = 128;    // tokens of a tile
+constexpr int kPlanThreads = 1024;
+// Members below which a prefix is not worth a pass of its own.
+constexpr int kMinMembers = 2;
+
+// A group's part of the prefix pass.
+struct GroupPlan {
+  int tile_base;  // tiles of the groups before it
+  int tiles;      // tiles of one unit (0: not shared)
+  int s_begin, s_end;
+  int leader;     // first member that covers the prefix: its table row is read
+  int prefix;     // tokens
+  int pad[2];
+};
+
+struct SharedParams {
+  const int32_t* group_start;
+  const int32_t* prefix_blocks;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  GroupPlan* groups;       // [G]
+  int* total;              // [1] tiles of the call
+  int32_t* seq_start;      // [S] first own position
+  int32_t* seq_group;      // [S] group, or -1
+  unsigned int* counters;  // the suffix pass's work counters
+  float* pre_o;            // [rows][D]
+  float2* pre_ml;          // [rows]
+  unsigned int* err;
+  int num_groups, num_seqs, num_heads, block_size, max_blocks, num_blocks, max_context_len;
+  int max_prefix_blocks, num_counters, workers, oob_row;
+  float scale_log2, v_scale;
+  // merge
+  void* out;
+  const float* suf_ml;
+  const float* suf_o;
+  int part_tokens, max_parts;
+};
+
+__device__ __forceinline__ int context_of(const SharedParams& a, int s) {
+  const long long cap = (long long)a.max_blocks * a.block_size;
+  int c = max(a.context_lens[s], 0);
+  if (c > cap) c = (int)cap;
+  return min(c, a.max_context_len);
+}
+
+// ---- plan -------------------------------------------------------------------
+
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams a) {
+  __shared__ long long sums[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int i = tid; i < a.num_counters; i += kPlanThreads) a.counters[i] = 0u;
+  for (int s = tid; s < a.num_seqs; s += kPlanThreads) {
+    a.seq_start[s] = 0;
+    a.seq_group[s] = -1;
+  }
+  // Bounds that do not increase would make groups overlap: nothing is shared.
+  bool bad = false;
+  for (int g = tid; g < a.num_groups; g += kPlanThreads) {
+    const int b = a.group_start[g], e = a.group_start[g + 1];
+    bad |= b < 0 || b > e || e > a.num_seqs || a.prefix_blocks[g] < 0;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) atomicOr(a.err, PA_ERRBIT_CONTEXT);
+  for (int g = warp; g < a.num_groups; g += kPlanThreads / 32) {
+    GroupPlan p{};
+    int blocks = 0, members = 0;
+    if (!bad) {
+      p.s_begin = a.group_start[g];
+      p.s_end = a.group_start[g + 1];
+      blocks = min(a.prefix_blocks[g], a.max_prefix_blocks);
+    }
+    p.prefix = blocks * a.block_size;
+    p.leader = -1;
+    if (blocks > 0)
+      for (int s0 = p.s_begin; s0 < p.s_end; s0 += 32) {
+        const int s = s0 + lane;
+        const unsigned in = __ballot_sync(kFullMask, s < p.s_end && context_of(a, s) >= p.prefix);
+        if (in != 0 && p.leader < 0) p.leader = s0 + __ffs(in) - 1;
+        members += __popc(in);
+      }
+    if (members >= kMinMembers) {
+      p.tiles = (p.prefix + kTile - 1) / kTile;
+      for (int s = p.s_begin + lane; s < p.s_end; s += 32)
+        if (context_of(a, s) >= p.prefix) {
+          a.seq_start[s] = p.prefix;
+          a.seq_group[s] = g;
+        }
+    }
+    if (lane == 0) a.groups[g] = p;
+  }
+  __syncthreads();
+  // Running sum of the groups' tiles.
+  long long carry = 0;
+  for (int base = 0; base < a.num_groups; base += kPlanThreads) {
+    const int g = base + tid;
+    long long n = 0;
+    if (g < a.num_groups) {
+      const GroupPlan p = a.groups[g];
+      n = (long long)p.tiles * ((p.s_end - p.s_begin + kRows - 1) / kRows) * a.num_heads;
+    }
+    long long x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(kFullMask, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    long long before = carry, all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) before += sums[w];
+      all += sums[w];
+    }
+    if (g < a.num_groups) a.groups[g].tile_base = (int)(before + x - n);
+    carry += all;
+  }
+  if (tid == 0) *a.total = (int)carry;
+}
+
+// ---- prefix pass ----------------------------------------------------------------
+
+__device__ __forceinline__ int active_workers(const SharedParams& a, int n) {
+  return max(1, min(a.workers, n));
+}
+__device__ __forceinline__ int worker_begin(int w, int W, int n) { return (int)((long long)w * n / W); }
+__device__ __forceinline__ int worker_of(int x, int W, int n) {
+  return (int)((((long long)x + 1) * W - 1) / n);
+}
+
+// A worker's walk over its tiles: unit by unit.  Every warp role walks by
+// itself.
+struct Walk {
+  int tile, left, g;        // next tile, tiles left, its group
+  int s0, rows, h;          // the current segment: first sequence, members, head
+  int t_begin, t_end, prefix, leader;
+  __device__ bool next(const SharedParams& a) {
+    if (left <= 0) return false;
+    GroupPlan p = a.groups[g];
+    auto tiles = [&] { return p.tiles * ((p.s_end - p.s_begin + kRows - 1) / kRows) * a.num_heads; };
+    while (tile >= p.tile_base + tiles()) {  // tile is below the total: ends
+      if (++g >= a.num_groups) return false;
+      p = a.groups[g];
+    }
+    const int u = (tile - p.tile_base) / p.tiles;
+    const int mt = u / a.num_heads;
+    h = u - mt * a.num_heads;
+    s0 = p.s_begin + mt * kRows;
+    rows = min(kRows, p.s_end - s0);
+    t_begin = tile - p.tile_base - u * p.tiles;
+    t_end = min(p.tiles, t_begin + left);
+    prefix = p.prefix;
+    leader = p.leader;
+    left -= t_end - t_begin;
+    tile += t_end - t_begin;
+    return true;
+  }
+};
+
+template <int D, bool F8>
+struct Traits {
+  static constexpr int NA = D / 64;             // swizzle atoms per row
+  static constexpr int ATOM = 128 * 128;        // 128 rows x 64 fp16
+  static constexpr int TB = kTile * D * 2;      // one fp16 tile of K or V (and the queries)
+  static constexpr int NST = F8 ? 2 : D == 128 ? 3 : 4;
+  static constexpr int CB = kTile * D;          // one tile of codes
+  static constexpr int NCS = F8 ? 2 : 0;        // stages of codes (K and V each)
+  static constexpr int OFF_K = TB;
+  static constexpr int OFF_V = OFF_K + NST * TB;
+  static constexpr int OFF_C = OFF_V + NST * TB;
+  static constexpr int OFF_BAR = OFF_C + NCS * 2 * CB;
+  static constexpr int USED = OFF_BAR + 512 + 1024;
+  // At least 120 KB, so that one CTA holds an SM (and its 512 TMEM columns).
+  static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
+  static_assert(SMEM <= 232448, "beyond the opt-in shared memory of one CTA");
+  static constexpr int THREADS = F8 ? 320 : 192;
+  static constexpr uint32_t COL_O = 256;        // S: 128 columns each; O: D columns
+};
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescale = 8.f;  // base-2 logits above the reference that move it
+
+// Barriers.
+enum {
+  kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = 6, kVFull = 10, kVEmpty = 14, kSFull = 18, kPFull = 20,
+  kOFull = 22, kDone = 23, kCFull = 24 /* K 24, 25; V 26, 27 */, kCEmpty = 28, kNumBars = 32
+};
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "  selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Polls two barriers (for at most the bounded wait's time): true when the
+// second one's phase is complete and the first one's is not.  Warp-uniform.
+__device__ __forceinline__ bool second_first(uint32_t a, uint32_t a_parity, uint32_t b, uint32_t b_parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    int r = mbar_test(a, a_parity) ? 1 : mbar_test(b, b_parity) ? 2 : 0;
+    if (r == 0 && global_timer_ns() - t0 > kWaitLimitNs) r = 1;  // the wait that follows reports it
+    r = __shfl_sync(kFullMask, r, 0);
+    if (r != 0) return r == 2;
+  }
+}
+
+// Widens one tile of codes (row-major) into the swizzled fp16 operand layout:
+// thread i of 128 takes 16-code column i % (D/16) of rows i / (D/16) + k * STEP.
+template <int D>
+__device__ __forceinline__ void widen(const unsigned char* src, unsigned char* dst, int i) {
+  constexpr int CPR = D / 16, STEP = 128 / CPR, ATOM = 128 * 128;
+  static_assert(STEP % 8 == 0, "a thread's rows share one swizzle phase");
+  const int j = i % CPR, r0 = i / CPR, c0 = 2 * (j % 4);
+  const unsigned char* sp = src + r0 * D + 16 * j;
+  unsigned char* dp = dst + (j / 4) * ATOM + r0 * 128;
+  const int o0 = (c0 ^ (r0 & 7)) << 4, o1 = ((c0 + 1) ^ (r0 & 7)) << 4;
+#pragma unroll 4
+  for (int k = 0; k < kTile / STEP; ++k) {
+    const uint4 c = lds128(sp + k * STEP * D);
+    *reinterpret_cast<uint4*>(dp + k * STEP * 128 + o0) = e4m3x8_to_f16x8(make_uint2(c.x, c.y));
+    *reinterpret_cast<uint4*>(dp + k * STEP * 128 + o1) = e4m3x8_to_f16x8(make_uint2(c.z, c.w));
+  }
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                         const __grid_constant__ CUtensorMap tv, const SharedParams a) {
+  using T = Traits<D, F8>;
+  constexpr int NST = T::NST;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s_base = smem_u32(sm);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + T::OFF_BAR);
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + T::OFF_BAR + 8 * kNumBars);
+  volatile int* fail = reinterpret_cast<volatile int*>(sm + T::OFF_BAR + 8 * kNumBars + 4);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 160) {
+    for (int i = 0; i < kNumBars; ++i) {
+      const bool by_wideners = F8 && ((i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) || i >= kCEmpty);
+      mbar_init(bar(i), i == kPFull || i == kPFull + 1 ? 128 : i == kDone ? T::THREADS : by_wideners ? 4 : 1);
+    }
+    *fail = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tq);
+    prefetch_tensormap(&tk);
+    prefetch_tensormap(&tv);
+  }
+  if (warp == 4) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int worker = blockIdx.x;
+  Walk w;
+  {
+    const int total = *a.total, W = active_workers(a, total);
+    w.tile = worker < W ? worker_begin(worker, W, total) : 0;
+    w.left = worker < W ? worker_begin(worker + 1, W, total) - w.tile : 0;
+    // The last group that starts at or before the tile and has any.
+    int lo = 0, hi = a.num_groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.groups[mid].tile_base <= w.tile) lo = mid; else hi = mid - 1;
+    }
+    // Groups without tiles share the base of the one after them: step back is
+    // never needed, since the search takes the last of equal bases, and that
+    // one holds the tile unless it is empty too, at the total's end.
+    w.g = lo;
+  }
+
+  if (warp == 4) {
+    // ---------------- TMA: a segment's queries, then its K and V tiles
+    const int bpt = kTile / a.block_size;
+    int g = 0, seg = 0, ki = 0, vi = 0;
+    bool ok = true;
+    auto uni = [&](bool v) { return __all_sync(kFullMask, v); };
+    while (ok && w.next(a)) {
+      if (seg > 0) ok = uni(mbar_wait_bounded(bar(kQEmpty), (seg - 1) & 1));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(kQFull), T::TB);
+#pragma unroll
+        for (int at = 0; at < T::NA; ++at)
+          tma_load_3d(s_base + at * T::ATOM, &tq, at * 64, w.h, w.s0, bar(kQFull));
+      }
+      __syncwarp();
+      ++seg;
+      const int32_t* bt = a.block_tables + (size_t)w.leader * a.max_blocks;
+      auto tile_row = [&](int t) {  // cache row of this lane's block, one tile ahead
+        const int lb = t * bpt + lane;
+        int row = a.oob_row;
+        if (lane < bpt && t < w.t_end && lb * a.block_size < w.prefix) {
+          const int phys = bt[lb];
+          if (phys >= 0 && phys < a.num_blocks)
+            row = (phys * a.num_heads + w.h) * a.block_size;
+          else
+            atomicOr(a.err, PA_ERRBIT_BLOCK_ID);
+        }
+        return row;
+      };
+      int row = tile_row(w.t_begin);
+      for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          uint32_t dst, full;
+          if constexpr (F8) {
+            const int st = g & 1;
+            if (g >= 2) ok = uni(mbar_wait_bounded(bar(kCEmpty + 2 * kv + st), ((g >> 1) - 1) & 1));
+            dst = s_base + T::OFF_C + (2 * kv + st) * T::CB;
+            full = bar(kCFull + 2 * kv + st);
+          } else {
+            const int st = g % NST;
+            if (g >= NST) ok = uni(mbar_wait_bounded(bar((kv ? kVEmpty : kKEmpty) + st), (g / NST - 1) & 1));
+            dst = s_base + (kv ? T::OFF_V : T::OFF_K) + st * T::TB;
+            full = bar((kv ? kVFull : kKFull) + st);
+          }
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(full, F8 ? T::CB : T::TB);
+          __syncwarp();
+          if (lane < bpt) {
+            if constexpr (F8) {
+              tma_load_2d(dst + lane * a.block_size * D, kv ? &tv : &tk, 0, row, full);
+            } else {
+#pragma unroll
+              for (int at = 0; at < T::NA; ++at)
+                tma_load_2d(dst + at * T::ATOM + lane * a.block_size * 128, kv ? &tv : &tk, at * 64, row, full);
+            }
+          }
+          ++(kv ? vi : ki);
+        }
+        if (!ok) break;
+        row = tile_row(t + 1);
+      }
+    }
+    if (!ok && lane == 0) {
+      *fail = 1;
+      // The copies in flight land (bounded) before the shared memory goes.
+      if (seg > 0) mbar_wait_bounded(bar(kQFull), (seg - 1) & 1);
+      constexpr int N = F8 ? 2 : NST;
+      for (int u = max(0, ki - N); u < ki; ++u)
+        mbar_wait_bounded(bar((F8 ? kCFull : kKFull) + u % N), (u / N) & 1);
+      for (int u = max(0, vi - N); u < vi; ++u)
+        mbar_wait_bounded(bar((F8 ? kCFull + 2 : kVFull) + u % N), (u / N) & 1);
+    }
+  } else if (warp == 5) {
+    // ---------------- MMA
+    constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
+    constexpr uint32_t kIdPV = umma_idesc_f16(kRows, D, false, true);
+    const bool leader = lane == 0;
+    const uint64_t q_desc = umma_desc_sw128(s_base, 16, 1024);
+    const uint64_t k_desc = umma_desc_sw128(s_base + T::OFF_K, 16, 1024);
+    const uint64_t v_desc = umma_desc_sw128(s_base + T::OFF_V, T::ATOM, 1024);
+    constexpr uint64_t kStep = (uint64_t)T::TB >> 4;
+    auto uni = [&](bool v) { return __all_sync(kFullMask, v); };
+    int qk = 0, pv = 0;
+    // P.V of tile g; `first`: it starts a segment.
+    auto pv_mma = [&](int g, bool first) {
+      bool ok = uni(mbar_wait_bounded(bar(kPFull + (g & 1)), (g >> 1) & 1));
+      ok = ok && uni(mbar_wait_bounded(bar(kVFull + g % NST), (g / NST) & 1));
+      if (!ok) return false;
+      tc_fence_after();
+      const uint64_t vd = v_desc + (g % NST) * kStep;
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        umma_f16_tmem_a_if(leader, tmem + T::COL_O, tmem + 128 * (g & 1) + 8 * k,
+                           vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV, !first || k > 0);
+      umma_commit_if(leader, bar(kVEmpty + g % NST));
+      umma_commit_if(leader, bar(kOFull));
+      ++pv;
+      return true;
+    };
+    int g = 0, seg = 0;
+    bool ok = true, prev_first = false;
+    while (ok && w.next(a)) {
+      ok = uni(mbar_wait_bounded(bar(kQFull), seg & 1));
+      for (int t = w.t_begin; ok && t < w.t_end; ++t, ++g) {
+        const int st = g % NST;
+        // Of S(t) and P.V of the tile before, the one that can start first.
+        if (g > 0 && second_first(bar(kKFull + st), (g / NST) & 1, bar(kPFull + ((g - 1) & 1)), ((g - 1) >> 1) & 1))
+          ok = pv_mma(g - 1, prev_first);
+        ok = ok && uni(mbar_wait_bounded(bar(kKFull + st), (g / NST) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t kd = k_desc + st * kStep;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = (uint64_t)(((k / 4) * T::ATOM + (k % 4) * 32) >> 4);
+          umma_f16_if(leader, tmem + 128 * (g & 1), q_desc + off, kd + off, kIdQK, k > 0);
+        }
+        umma_commit_if(leader, bar(kSFull + (g & 1)));
+        umma_commit_if(leader, bar(kKEmpty + st));
+        ++qk;
+        if (t + 1 == w.t_end) umma_commit_if(leader, bar(kQEmpty));  // the queries' last reader
+        if (pv < g) ok = pv_mma(g - 1, prev_first);
+        prev_first = t == w.t_begin;
+      }
+      ++seg;
+    }
+    if (ok && g > 0) ok = pv_mma(g - 1, prev_first);
+    if (!ok && lane == 0) {
+      atomicOr(a.err, PA_ERRBIT_TIMEOUT);
+      *fail = 1;
+      // Every product started ends (bounded) before its memory goes.
+      if (qk > 0) mbar_wait_bounded(bar(kSFull + ((qk - 1) & 1)), ((qk - 1) >> 1) & 1);
+      if (pv > 0) mbar_wait_bounded(bar(kOFull), (pv - 1) & 1);
+    }
+  } else if (warp < 4) {
+    // ---------------- softmax: one query row a thread
+    const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
+    const int row = tid;
+    int g = 0;
+    bool ok = true;
+    while (ok && w.next(a)) {
+      const bool live = warp * 32 < w.rows;  // this warp has members
+      float m = -INFINITY, l = 0.f;
+      for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
+        const uint32_t t_s = tmem + t_lane + 128 * (g & 1);
+        ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kSFull + (g & 1)), (g >> 1) & 1) && !*fail);
+        if (!ok) break;
+        if (live) {
+          tc_fence_after();
+          float x[kTile];
+          {
+            uint32_t sr[kTile];
+#pragma unroll
+            for (int cb = 0; cb < kTile / 32; ++cb)
+              tmem_ld32(t_s + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cb * 32]));
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) x[j] = __uint_as_float(sr[j]) * a.scale_log2;
+          }
+          const int lim = w.prefix - t * kTile;  // the prefix may end inside the tile
+          if (lim < kTile) {
+#pragma unroll
+            for (int j = 0; j < kTile; ++j)
+              if (j >= lim) x[j] = -INFINITY;
+          }
+          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < kTile; j += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mq[u] = fmax3(mq[u], x[j + 2 * u], x[j + 2 * u + 1]);
+          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+          float alpha = 1.f;
+          if (mx > m + kRescale || m == -INFINITY) {
+            alpha = m == -INFINITY ? 1.f : exp2_approx(m - mx);
+            m = mx;
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          uint32_t pk[kTile / 2];
+          float sq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < kTile / 2; ++j) {
+            pk[j] = exp2_f32_to_f16x2(x[2 * j] - ref, x[2 * j + 1] - ref);
+            sq[j & 3] = add_f16x2_f32(pk[j], sq[j & 3]);
+          }
+          l = l * alpha + ((sq[0] + sq[1]) + (sq[2] + sq[3]));
+          if (t > w.t_begin && __any_sync(kFullMask, alpha != 1.f)) {
+            // O holds the tiles up to t - 1 once P.V of t - 1 is done.
+            ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kOFull), (g - 1) & 1) && !*fail);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int cb = 0; cb < D / 32; ++cb) {
+              uint32_t r[32];
+              tmem_ld32(tmem + t_lane + T::COL_O + cb * 32, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+              tmem_st32(tmem + t_lane + T::COL_O + cb * 32, r);
+            }
+          }
+          // P over the first 64 columns of its S.
+#pragma unroll
+          for (int cb = 0; cb < 2; ++cb)
+            tmem_st32(t_s + cb * 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[cb * 32]));
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        mbar_arrive(bar(kPFull + (g & 1)));
+      }
+      if (!ok) break;
+      // The segment's partial rows.
+      ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kOFull), (g - 1) & 1) && !*fail);
+      if (!ok) break;
+      if (live) {
+        tc_fence_after();
+        const size_t pr = (size_t)a.num_heads * w.s0 + (size_t)w.h * w.rows + (size_t)worker * kRows + row;
+        if (row < w.rows) a.pre_ml[pr] = make_float2(m, l);
+#pragma unroll
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t r[32];
+          tmem_ld32(tmem + t_lane + T::COL_O + cb * 32, r);
+          tmem_wait_ld();
+          if (row < w.rows) {
+            float* o = a.pre_o + pr * D + cb * 32;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(o + j) =
+                  make_float4(__uint_as_float(r[j]) * a.v_scale, __uint_as_float(r[j + 1]) * a.v_scale,
+                              __uint_as_float(r[j + 2]) * a.v_scale, __uint_as_float(r[j + 3]) * a.v_scale);
+          }
+        }
+        tc_fence_before();
+      }
+    }
+    if (!ok && lane == 0) *fail = 1;
+  } else if constexpr (F8) {
+    // ---------------- E4M3 caches: four warps widen the staged codes
+    const int i = tid - 192;
+    int g = 0;
+    bool ok = true;
+    while (ok && w.next(a)) {
+      for (int t = w.t_begin; ok && t < w.t_end; ++t, ++g) {
+        const int cs = g & 1, st = g % NST;
+#pragma unroll
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          ok = mbar_wait_bounded(bar(kCFull + 2 * kv + cs), (g >> 1) & 1);
+          if (g >= NST) ok = ok && mbar_wait_bounded(bar((kv ? kVEmpty : kKEmpty) + st), (g / NST - 1) & 1);
+          ok = __all_sync(kFullMask, ok && !*fail);
+          if (!ok) break;
+          widen<D>(sm + T::OFF_C + (2 * kv + cs) * T::CB, sm + (kv ? T::OFF_V : T::OFF_K) + st * T::TB, i);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(kCEmpty + 2 * kv + cs));
+            mbar_arrive(bar((kv ? kVFull : kKFull) + st));
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) *fail = 1;
+  }
+  tc_fence_before();
+  mbar_arrive(bar(kDone));
+  if (warp == 4) {
+    if (!mbar_wait_bounded(bar(kDone), 0) && lane == 0) atomicOr(a.err, PA_ERRBIT_TIMEOUT);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---- merge -------------------------------------------------------------------
+
+// One warp a (sequence, head), D/32 values a lane: the prefix's partials, then
+// the suffix's, in that order.
+template <int D>
+__global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams a) {
+  constexpr int N = D / 32;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long pair = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (pair >= (long long)a.num_seqs * a.num_heads) return;
+  const int s = (int)(pair / a.num_heads), h = (int)(pair - (long long)s * a.num_heads);
+  const int c = context_of(a, s), start = a.seq_start[s], g = a.seq_group[s];
+  const int n_suf = c > start ? (c - start + a.part_tokens - 1) / a.part_tokens : 0;
+  int n_pre = 0;
+  size_t pre0 = 0;
+  if (g >= 0) {
+    const GroupPlan p = a.groups[g];
+    const int total = *a.total, W = active_workers(a, total);
+    const int mt = (s - p.s_begin) / kRows, s0 = p.s_begin + mt * kRows;
+    const int rows = min(kRows, p.s_end - s0);
+    const int t0 = p.tile_base + (mt * a.num_heads + h) * p.tiles;
+    const int w0 = worker_of(t0, W, total), w1 = worker_of(t0 + p.tiles - 1, W, total);
+    n_pre = w1 - w0 + 1;
+    pre0 = (size_t)a.num_heads * s0 + (size_t)h * rows + (size_t)w0 * kRows + (s - s0);
+  }
+  const int n = n_pre + n_suf;
+  const size_t suf0 = (size_t)pair * a.max_parts;
+  auto ml_of = [&](int i) {
+    return i < n_pre ? a.pre_ml[pre0 + (size_t)i * kRows]
+                     : reinterpret_cast<const float2*>(a.suf_ml)[suf0 + (i - n_pre)];
+  };
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, ml_of(i).x);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+  float L = 0.f, acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  for (int base = 0; base < n; base += 32) {
+    float wt = 0.f, wl = 0.f;
+    if (base + lane < n) {
+      const float2 ml = ml_of(base + lane);
+      wt = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - M);
+      wl = wt * ml.y;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) wl += __shfl_xor_sync(kFullMask, wl, o);
+    L += wl;
+    const int cnt = min(32, n - base);
+#pragma unroll 4
+    for (int j = 0; j < cnt; ++j) {
+      const int i = base + j;
+      const float* src = (i < n_pre ? a.pre_o + (pre0 + (size_t)i * kRows) * D
+                                    : a.suf_o + (suf0 + (i - n_pre)) * D) + lane * N;
+      const float x = __shfl_sync(kFullMask, wt, j);
+      if constexpr (N == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        acc[0] = fmaf(x, v.x, acc[0]);
+        acc[1] = fmaf(x, v.y, acc[1]);
+        acc[2] = fmaf(x, v.z, acc[2]);
+        acc[3] = fmaf(x, v.w, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(x, v.x, acc[0]);
+        acc[1] = fmaf(x, v.y, acc[1]);
+      }
+    }
+  }
+  __half* out = static_cast<__half*>(a.out) + (size_t)pair * D + lane * N;
+#pragma unroll
+  for (int i = 0; i < N; i += 2)
+    *reinterpret_cast<__half2*>(out + i) =
+        __floats2half2_rn(L > 0.f ? acc[i] / L : 0.f, L > 0.f ? acc[i + 1] / L : 0.f);
+}
+
+struct Layout {
+  size_t total, groups, start, group, ml, o, bytes;
+};
+
+Layout layout(int S, int G, int H, int D, int sms) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  Layout l{};
+  const size_t rows = (size_t)S * H + (size_t)sms * kRows;
+  l.total = 0;
+  l.groups = 256;
+  l.start = up(l.groups + (size_t)G * sizeof(GroupPlan));
+  l.group = up(l.start + (size_t)S * 4);
+  l.ml = up(l.group + (size_t)S * 4);
+  l.o = up(l.ml + rows * sizeof(float2));
+  l.bytes = up(l.o + rows * D * sizeof(float));
+  return l;
+}
+
+SharedParams params(const SharedArgs& g) {
+  const Layout l = layout(g.num_seqs, g.num_groups, g.dec.num_heads, g.head_dim, g.sms);
+  SharedParams p{};
+  p.group_start = g.group_start;
+  p.prefix_blocks = g.prefix_blocks;
+  p.block_tables = g.dec.block_tables;
+  p.context_lens = g.dec.context_lens;
+  p.total = reinterpret_cast<int*>(g.workspace + l.total);
+  p.groups = reinterpret_cast<GroupPlan*>(g.workspace + l.groups);
+  p.seq_start = reinterpret_cast<int32_t*>(g.workspace + l.start);
+  p.seq_group = reinterpret_cast<int32_t*>(g.workspace + l.group);
+  p.pre_ml = reinterpret_cast<float2*>(g.workspace + l.ml);
+  p.pre_o = reinterpret_cast<float*>(g.workspace + l.o);
+  p.counters = g.dec.counter;
+  p.err = g.dec.err;
+  p.num_groups = g.num_groups;
+  p.num_seqs = g.num_seqs;
+  p.num_heads = g.dec.num_heads;
+  p.block_size = g.block_size;
+  p.max_blocks = g.dec.max_blocks;
+  p.num_blocks = g.dec.num_blocks;
+  p.max_context_len = g.dec.max_context_len;
+  // Blocks of 4 tokens are half a swizzle atom: their prefixes stay in the
+  // suffix pass.
+  const int mp = g.max_prefix_len / g.block_size;
+  p.max_prefix_blocks = g.block_size < 8 ? 0 : mp < g.dec.max_blocks ? mp : g.dec.max_blocks;
+  p.num_counters = g.num_counters;
+  p.workers = g.sms;
+  p.scale_log2 = g.dec.scale_log2;
+  p.v_scale = g.fp8 ? g.dec.v_scale : 1.f;
+  p.out = g.dec.out;
+  p.suf_ml = g.dec.ws_ml;
+  p.suf_o = g.dec.ws_o;
+  p.part_tokens = g.dec.part_tokens;
+  p.max_parts = g.dec.max_parts;
+  return p;
+}
+
+template <int D, bool F8>
+cudaError_t launch_prefix_t(const SharedArgs& g, SharedParams p, cudaStream_t stream) {
+  using T = Traits<D, F8>;
+  static std::atomic<unsigned long long> prepared{0};  // per device: the shared-memory opt-in
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev > 63 || !(prepared.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(shared_prefix_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev <= 63) prepared.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  const int H = g.dec.num_heads;
+  const long long rows = (long long)g.dec.num_blocks * H * g.block_size;
+  p.oob_row = (int)rows;
+  CUtensorMap tq, tk, tv;
+  const cuuint64_t qdims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)g.num_seqs};
+  const cuuint64_t qstr[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
+  const cuuint32_t qbox[3] = {64, 1, (cuuint32_t)kRows};
+  const cuuint64_t kdims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  const cuuint64_t kstr[1] = {(cuuint64_t)D * (F8 ? 1 : 2)};
+  const cuuint32_t kbox[2] = {(cuuint32_t)(F8 ? D : 64), (cuuint32_t)g.block_size};
+  if (!encode_tensor_map(&tq, g.dec.query, 3, qdims, qstr, qbox) ||
+      !encode_tensor_map(&tk, g.dec.key_cache, 2, kdims, kstr, kbox, F8) ||
+      !encode_tensor_map(&tv, g.dec.value_cache, 2, kdims, kstr, kbox, F8))
+    return cudaErrorInvalidValue;
+  return launch_pdl(shared_prefix_kernel<D, F8>, dim3(p.workers), dim3(T::THREADS), T::SMEM, stream, tq, tk,
+                    tv, p);
+}
+
+}  // namespace
+
+size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_heads, int head_dim, int sms) {
+  return layout(num_seqs, num_groups, num_heads, head_dim, sms).bytes;
+}
+
+cudaError_t launch_shared_prefix(SharedArgs& g, cudaStream_t stream) {
+  const SharedParams p = params(g);
+  g.dec.seq_start = p.seq_start;
+  const cudaError_t e = launch_pdl(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+  if (e != cudaSuccess || p.num_groups == 0 || p.max_prefix_blocks == 0) return e;
+  if (g.fp8)
+    return g.head_dim == 64 ? launch_prefix_t<64, true>(g, p, stream) : launch_prefix_t<128, true>(g, p, stream);
+  return g.head_dim == 64 ? launch_prefix_t<64, false>(g, p, stream) : launch_prefix_t<128, false>(g, p, stream);
+}
+
+cudaError_t launch_shared_merge(const SharedArgs& g, cudaStream_t stream) {
+  const SharedParams p = params(g);
+  const long long warps = (long long)g.num_seqs * g.dec.num_heads;
+  const dim3 grid((unsigned)((warps + 3) / 4));
+  return g.head_dim == 64 ? launch_pdl(shared_merge_kernel<64>, grid, dim3(128), 0, stream, p)
+                          : launch_pdl(shared_merge_kernel<128>, grid, dim3(128), 0, stream, p);
+}
+
+}  // namespace pa

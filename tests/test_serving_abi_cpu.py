@@ -1,4 +1,4 @@
-"""Refusals of the table build and the latent cache's calls, on the host,
+"""Refusals of the table build, the shared-prefix decode and the latent cache's calls, on the host,
 before any CUDA call."""
 import ctypes
 import os
@@ -19,6 +19,10 @@ def lib():
     x.pa_latent_decode_workspace_size.restype = sz
     x.pa_build_tables.argtypes = [vp, i32, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32,
                                   i32, i32, vp, sz, vp]
+    x.pa_decode_shared_workspace_size.restype = sz
+    x.pa_decode_shared.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp] + [i32] * 6 + [f32, i32, i32, vp, sz, vp]
+    x.pa_decode_shared_fp8.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp] + [i32] * 6 + [f32, f32, f32, i32,
+                                                                                      i32, vp, sz, vp]
     x.pa_latent_write.argtypes = [vp, i64, vp, i64, vp, vp, i32, i32, i32, i32, i32, vp]
     x.pa_latent_decode.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp,
                                    sz, vp]
@@ -76,7 +80,40 @@ def test_latent_write_refusals(lib, change, status):
     assert lib.pa_latent_write(*dict(a, **change).values()) == status
 
 
+SHARED = dict(out=P[0], q=P[1], k=P[2], v=P[3], bt=P[4], max_blocks=8, ctx=P[5], starts=P[6], pre=P[7],
+              groups=2, seqs=4, heads=8, D=128, block_size=16, num_blocks=64, scale=0.1)
+SHARED_TAIL = dict(max_len=100, max_prefix=32, ws=P[8], ws_bytes=1 << 34, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(D=96), UNSUPPORTED), (dict(block_size=64), UNSUPPORTED), (dict(groups=-1), INVALID),
+    (dict(groups=5), INVALID), (dict(seqs=-1), INVALID), (dict(heads=0), INVALID), (dict(num_blocks=0), INVALID),
+    (dict(max_blocks=0), INVALID), (dict(max_len=-1), INVALID), (dict(max_prefix=-1), INVALID),
+    (dict(out=None), INVALID), (dict(q=P[1] + 8), INVALID), (dict(k=None), INVALID), (dict(v=P[3] + 2), INVALID),
+    (dict(bt=P[4] + 1), INVALID), (dict(ctx=None), INVALID), (dict(starts=None), INVALID),
+    (dict(pre=P[7] + 2), INVALID), (dict(ws=None), INVALID), (dict(ws=P[8] + 8), INVALID),
+    (dict(ws_bytes=1 << 10), INVALID), (dict(num_blocks=1 << 24), UNSUPPORTED),
+    (dict(max_prefix=2 ** 31 - 1, heads=128), UNSUPPORTED), (dict(seqs=0, out=None), OK),
+])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_shared_refusals(lib, fp8, change, status):
+    a = {k: change.get(k, v) for k, v in SHARED.items()}
+    b = {k: change.get(k, v) for k, v in SHARED_TAIL.items()}
+    if fp8:
+        assert lib.pa_decode_shared_fp8(*a.values(), 0.5, 0.25, *b.values()) == status
+        if status == OK:
+            for ks, vs in ((0.0, 1.0), (1.0, -1.0), (float("inf"), 1.0), (1.0, float("nan"))):
+                assert lib.pa_decode_shared_fp8(*a.values(), ks, vs, *b.values()) == INVALID
+    else:
+        assert lib.pa_decode_shared(*a.values(), *b.values()) == status
+
+
 def test_workspace_sizes(lib):
+    size = lib.pa_decode_shared_workspace_size
+    assert size(4, 1, 8, 128, 100, 32) > 0 == size(4, 1, 8, 96, 100, 32)
+    assert size(-1, 1, 8, 128, 100, 32) == size(4, 1, 0, 128, 100, 32) == size(4, 1, 8, 128, -1, 32) == 0
+    # the prefix's partial rows: one for each (sequence, head), 128 more for each SM
+    assert size(64, 1, 32, 128, 2048, 512) >= (64 * 32 + 152 * 128) * 128 * 4
     assert lib.pa_build_tables_workspace_size(-1) == 0 and lib.pa_build_tables_workspace_size(0) > 0
     assert lib.pa_build_tables_workspace_size(100) >= 100 * 20
     assert lib.pa_latent_decode_workspace_size(-1, 16) == 0 == lib.pa_latent_decode_workspace_size(4, 0)
