@@ -14,33 +14,39 @@
 // with 128 heads 242: HBM and tensor cores together.
 //
 // Design (GB300):
-//  * One persistent CTA per SM takes (64 heads) x (a range of 64-token tiles):
-//    the batch's tiles, numbered sequence by sequence, are cut into equal
-//    ranges, one for each worker, so ragged batches and single long contexts
-//    alike load every SM to within a tile.  More than 64 heads: the CTAs of
-//    one worker (one for each 64 heads) walk the same range at the same time,
-//    so the rows come from HBM once and from L2 for the others.
+//  * A cluster of two CTAs takes (128 heads) x (a range of 64-token tiles): the
+//    batch's tiles, numbered sequence by sequence, are cut into equal ranges,
+//    one for each cluster, so ragged batches and single long contexts alike
+//    load every SM to within a tile.  More than 128 heads: the clusters of one
+//    worker (one for each 128 heads) walk the same range at the same time, so
+//    the rows come from HBM once and from L2 for the others.
 //  * Worker w's part of sequence s is at most one segment; its partial result
 //    (m, l, o) goes to slot s + w of the workspace (along the walk either s or
 //    w grows, so the slots are distinct and there are at most S + W), and a
 //    merge kernel joins a sequence's segments.  A sequence inside one range is
 //    written directly.
-//  * 64 heads are the rows of the products (M = 64) because of the memories:
-//    the output of 128 heads x 512 fp32 would fill the tensor memory with no
-//    room for logits, and 128 query rows the shared memory with no room for
-//    two tiles.  With M = 64 an accumulator uses 16 of every 32 lanes: the
-//    output's first 256 values sit in lanes 0-15 and the last 256 in lanes
-//    16-31 of the same 256 columns.
-//  * A tile is 64 rows of 576 values (nine 64-value swizzle atoms), copied by
-//    TMA one box a block and atom into a two-stage ring; it is the K operand
-//    of S = Q K^T (N = 64) and, its first eight atoms read the other way
-//    round, the V operand of O += P V (N = 256, twice).
-//  * Four softmax warps (one head row a lane) read S from tensor memory, keep
-//    the running reference and sum in fp32 and write P, rounded once to fp16
-//    (the sum adds the rounded weights), to shared memory.  The reference
-//    moves only when the tile's maximum is more than 2^8 above it, so the
-//    output in tensor memory is seldom rescaled.
-//  * S is double-buffered: S(t+1) is computed while the softmax works on S(t).
+//  * The two CTAs split the row's values, not the tokens: CTA r holds latent
+//    values [256 r, 256 r + 256) and contracts those and half of the rotary
+//    ones, so S = Q K^T is the sum of two halves, exchanged through
+//    distributed shared memory (st.async, 32 KB a tile and direction); each
+//    CTA then computes the same weights P and O += P V for its 256 values.
+//    The reason is the tensor memory: 128 rows x 512 fp32 of output would fill
+//    it.  (64 heads a CTA with all 512 values in 256 columns x both halves of
+//    the lanes were built first: M = 64 products take as long as M = 128 ones,
+//    a tile cost 1.3 us for Q K^T and 0.65 us for P V, and 64 sequences of
+//    4096-8192 tokens with 128 heads took 246 us.)
+//  * The queries (fp16, 144 columns) are the A operand of Q K^T from tensor
+//    memory, so a product of 64 tokens reads 2 KB of shared memory, not 6, and
+//    the shared memory holds four stages of rows.
+//  * A stage is 64 rows of the CTA's 256 latent values and the 64 rotary ones
+//    (five 64-value swizzle atoms), copied by TMA one box a block and atom; it
+//    is the K operand of Q K^T and, its first four atoms read the other way
+//    round, the V operand of P V.
+//  * Four softmax warps (one head row a thread) send their half of S(t + 1)
+//    before they work on S(t), so the exchange overlaps the softmax.  Running
+//    reference and sum are fp32, P is rounded once to fp16 (the sum adds the
+//    rounded weights).  The reference moves only when the tile's maximum is
+//    more than 2^8 above it, so the output is seldom rescaled.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -86,29 +92,38 @@ __global__ void __launch_bounds__(256)
 
 // ---- decode -----------------------------------------------------------------
 
-constexpr int kRows = 64;              // head rows of a CTA (MMA M)
+constexpr int kRows = 128;             // head rows of a cluster (MMA M)
 constexpr int kTile = 64;              // tokens of a tile
-constexpr int kAtoms = kLatentRow / 64;
-constexpr int kAtomBytes = 64 * 128;   // 64 rows x 64 fp16
-constexpr int kTileBytes = kAtoms * kAtomBytes;
+constexpr int kHalf = kLatentDim / 2;  // output values of a CTA
+constexpr int kAtoms = 5;              // its 64-value atoms: four latent, the rotary one
+constexpr int kAtomBytes = kTile * 128;
+constexpr int kStageBytes = kAtoms * kAtomBytes;
+constexpr int kStages = 4;
 constexpr int kThreads = 192;          // four softmax warps, TMA, MMA
 constexpr int kSeqsPerLaunch = 1024;
 
-constexpr int kOffQ = 0;
-constexpr int kOffK = kTileBytes;      // stage s at kOffK + s * kTileBytes
-constexpr int kOffP = 3 * kTileBytes;
-constexpr int kOffBar = kOffP + kAtomBytes;
-constexpr int kSmem = kOffBar + 256 + 1024;  // + alignment slack
+constexpr int kXBytes = kRows * kTile * 4;                 // one half of S from the other CTA
+constexpr int kOffX = kStages * kStageBytes;               // buffer b at kOffX + b * kXBytes
+constexpr int kOffBar = kOffX + 2 * kXBytes;
+constexpr int kSmem = kOffBar + 256 + 1024;                // + alignment slack
 static_assert(kSmem <= 232448, "beyond the opt-in shared memory of one CTA");
 
-constexpr uint32_t kTmemCols = 512;    // O: [0, 256); S: 64 columns each
-constexpr uint32_t kColS = 256;
-constexpr uint32_t kLaneHi = 16u << 16;  // the output's upper 256 values
+constexpr uint32_t kTmemCols = 512;    // O: [0, 256)
+constexpr uint32_t kColQ = 256;        // queries: 128 columns latent, 16 rotary (and 16 unused)
+constexpr uint32_t kColS = 416;        // 64
+constexpr uint32_t kColP = 480;        // 32
 
 constexpr float kRescale = 8.f;        // base-2 logits above the reference that move it
 
+// Barriers.
+enum {
+  kKFull = 0, kKEmpty = 4, kQFull = 8, kSFull = 9, kSFree = 10, kPFull = 11, kOFull = 12, kXFull = 13 /* 2 */,
+  kXFree = 15 /* 2 */, kDone = 17, kNumBars = 18
+};
+
 struct LatentParams {
   void* out;
+  const void* query;
   const int32_t* block_tables;
   const int32_t* context_lens;
   float* ws_o;       // [slots][H][512]
@@ -183,40 +198,79 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Polls two barriers (for at most the bounded wait's time): true when the
-// second one's phase is complete and the first one's is not.  Warp-uniform.
-__device__ __forceinline__ bool pv_first(uint32_t tile, uint32_t tile_parity, uint32_t p,
-                                         uint32_t p_parity) {
+// ---- the other CTA of the cluster -------------------------------------------
+
+__device__ __forceinline__ uint32_t peer_address(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+// 16 bytes to the other CTA's shared memory, counted on its barrier.
+__device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, uint32_t x, uint32_t y, uint32_t z,
+                                       uint32_t w) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+      "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// An arrival on the other CTA's barrier that orders nothing by itself.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Bounded wait on a barrier that the other CTA completes.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
   while (true) {
-    int r = mbar_test(tile, tile_parity) ? 1 : mbar_test(p, p_parity) ? 2 : 0;
-    if (r == 0 && global_timer_ns() - t0 > kWaitLimitNs) r = 1;  // the wait that follows reports it
-    r = __shfl_sync(kFullMask, r, 0);
-    if (r != 0) return r == 2;
+    uint32_t ok;
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "  selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
   }
 }
 
+// Both CTAs reach it: every wait before it is bounded.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_decode_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tc,
-                         const LatentParams a) {
+    latent_decode_kernel(const __grid_constant__ CUtensorMap tc, const LatentParams a) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t s_base = smem_u32(sm);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
-  // 0 q_full, 1 q_empty, 2,3 k_full, 4,5 k_empty, 6,7 s_full, 8 p_full, 9 o_full, 10 done
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kOffBar + 128);
-  volatile int* fail = reinterpret_cast<volatile int*>(sm + kOffBar + 132);
-  int* start = reinterpret_cast<int*>(sm + kOffBar + 136);  // first sequence, its first tile, tiles
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kOffBar + 8 * kNumBars);
+  volatile int* fail = reinterpret_cast<volatile int*>(sm + kOffBar + 8 * kNumBars + 4);
+  int* start = reinterpret_cast<int*>(sm + kOffBar + 8 * kNumBars + 8);  // first sequence, its first tile, tiles
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = blockIdx.x & 1;
+  const int cluster = (int)blockIdx.x >> 1;
+  const int worker = cluster / a.head_tiles, ht = cluster % a.head_tiles;
+  const int h0 = ht * kRows;
+  const int live_warps = min(4, (a.num_heads - h0 + 31) / 32);  // softmax warps with heads
   if (tid == 160) {
-    for (int i = 0; i < 10; ++i) mbar_init(bar(i), i == 8 ? 128 : 1);
-    mbar_init(bar(10), kThreads);
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(bar(i), i == kQFull || i == kSFree || i == kPFull ? 128
+                        : i == kXFree || i == kXFree + 1          ? live_warps
+                        : i == kDone                              ? kThreads
+                                                                  : 1);
     *fail = 0;
     fence_mbar_init();
-    prefetch_tensormap(&tq);
     prefetch_tensormap(&tc);
   }
   if (warp == 4) {
@@ -227,7 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   // Tiles of every sequence and this worker's first: warp 0 scans 32 lengths
   // at a time.
-  const int worker = (int)blockIdx.x / a.head_tiles, ht = (int)blockIdx.x % a.head_tiles;
   if (warp == 0) {
     int total = 0;
     const bool first = blockIdx.x == 0;
@@ -265,30 +318,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // the other CTA's barriers exist
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Walk w;
   w.s = start[0];
   w.t = start[1];
   w.left = start[2];
-  const int h0 = ht * kRows;
+  const int n_tiles = w.left;
 
   if (warp == 4) {
-    // ---------------- TMA: the queries of a segment, then its tiles
+    // ---------------- TMA: the tiles of the range
     const int nb = kTile / a.block_size;
-    int g = 0, seg = 0;
+    const int b = lane % nb;
+    int g = 0;
     bool ok = true;
     while (ok && w.next(a)) {
-      if (seg > 0) ok = __all_sync(kFullMask, mbar_wait_bounded(bar(1), (seg - 1) & 1));
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(bar(0), kTileBytes);
-      __syncwarp();
-      if (lane < kAtoms)
-        tma_load_2d(s_base + kOffQ + lane * kAtomBytes, &tq, lane * 64,
-                    (a.seq_begin + w.cur) * a.num_heads + h0, bar(0));
-      ++seg;
       const int32_t* bt = a.block_tables + (size_t)(a.seq_begin + w.cur) * a.max_blocks;
-      const int b = lane % nb;
       // The cache row of this lane's block of tile t, one tile ahead.
       auto tile_row = [&](int t) {
         const int lb = t * nb + b;
@@ -297,22 +343,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int phys = bt[lb];
           if (phys >= 0 && phys < a.num_blocks)
             row = phys * a.block_size;
-          else if (lane < nb)
+          else if (lane < nb && rank == 0)
             atomicOr(a.err, PA_ERRBIT_BLOCK_ID);
         }
         return row;
       };
       int row = tile_row(w.t_begin);
       for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
-        const int st = g & 1;
-        if (g >= 2) ok = __all_sync(kFullMask, mbar_wait_bounded(bar(4 + st), ((g >> 1) - 1) & 1));
+        const int st = g % kStages;
+        if (g >= kStages)
+          ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kKEmpty + st), (g / kStages - 1) & 1));
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(2 + st), kTileBytes);
+        if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + st), kStageBytes);
         __syncwarp();
-        const uint32_t dst = s_base + kOffK + st * kTileBytes + b * a.block_size * 128;
+        const uint32_t dst = s_base + st * kStageBytes + b * a.block_size * 128;
         for (int i = lane; i < kAtoms * nb; i += 32) {
           const int at = i / nb;
-          tma_load_2d(dst + at * kAtomBytes, &tc, at * 64, row, bar(2 + st));
+          tma_load_2d(dst + at * kAtomBytes, &tc, at < 4 ? (int)rank * kHalf + at * 64 : kLatentDim, row,
+                      bar(kKFull + st));
         }
         row = tile_row(t + 1);
       }
@@ -320,198 +368,267 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) {
       *fail = 1;
       // The copies in flight land (bounded) before the shared memory goes.
-      if (seg > 0) mbar_wait_bounded(bar(0), (seg - 1) & 1);
-      for (int u = max(0, g - 2); u < g; ++u) mbar_wait_bounded(bar(2 + (u & 1)), (u >> 1) & 1);
+      for (int u = max(0, g - kStages); u < g; ++u)
+        mbar_wait_bounded(bar(kKFull + u % kStages), (u / kStages) & 1);
     }
   } else if (warp == 5) {
-    // ---------------- MMA: S(t + 1) before P.V of t, so the softmax of t
-    // overlaps a product
+    // ---------------- MMA: S of tile i and P.V of tile j, whichever can start.
+    // S has one buffer (the softmax takes it to registers), P another.
     constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
-    constexpr uint32_t kIdPV = umma_idesc_f16(kRows, 256, false, true);
-    const bool leader = lane == 0;
-    const uint64_t q_desc = umma_desc_sw128(s_base + kOffQ, 16, 1024);
-    const uint64_t k_desc = umma_desc_sw128(s_base + kOffK, 16, 1024);
-    const uint64_t v_desc = umma_desc_sw128(s_base + kOffK, kAtomBytes, 1024);
-    const uint64_t p_desc = umma_desc_sw128(s_base + kOffP, 16, 1024);
-    constexpr uint64_t kStageStep = (uint64_t)kTileBytes >> 4;
-    auto uni = [&](bool v) { return __all_sync(kFullMask, v); };
-    // P.V of tile g; `first`: it starts a segment.
-    int qk = 0, pv = 0;
-    auto pv_mma = [&](int g, bool first) {
-      const uint64_t vd = v_desc + (g & 1) * kStageStep;
-      tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-          umma_f16_if(leader, tmem + (half ? kLaneHi : 0u), p_desc + (uint64_t)((k * 32) >> 4),
-                      vd + (uint64_t)((half * 4 * kAtomBytes + k * 16 * 128) >> 4), kIdPV,
-                      !first || k > 0);
-      umma_commit_if(leader, bar(4 + (g & 1)));
-      umma_commit_if(leader, bar(9));
-      ++pv;
-    };
-    int g = 0, seg = 0;
-    bool ok = true, prev_first = false;
-    while (ok && w.next(a)) {
-      ok = uni(mbar_wait_bounded(bar(0), seg & 1));
-      for (int t = w.t_begin; ok && t < w.t_end; ++t, ++g) {
-        const int st = g & 1;
-        // Of S(t) and P.V of the tile before, the one that can start first: a
-        // tile that is still on its way must not hold back the product that
-        // frees the other stage.
-        if (g > 0 && pv_first(bar(2 + st), (g >> 1) & 1, bar(8), (g - 1) & 1)) {
-          ok = uni(mbar_wait_bounded(bar(8), (g - 1) & 1));
-          if (ok) pv_mma(g - 1, prev_first);
+    constexpr uint32_t kIdPV = umma_idesc_f16(kRows, kHalf, false, true);
+    const uint64_t k_desc = umma_desc_sw128(s_base, 16, 1024);
+    const uint64_t v_desc = umma_desc_sw128(s_base, kAtomBytes, 1024);
+    constexpr uint64_t kStep = (uint64_t)kStageBytes >> 4;
+    int i = 0, j = 0, seg = 0, t = 0;
+    unsigned firsts = 0;  // bit j % 32: tile j starts a segment
+    w.t_end = 0;
+    bool ok = true;
+    uint64_t t0 = global_timer_ns();
+    while (j < n_tiles) {
+      // 1: S(i) can start; 2: P.V(j) can.
+      int r = 0;
+      if (i < n_tiles && mbar_test(bar(kKFull + i % kStages), (i / kStages) & 1) &&
+          (i == 0 || mbar_test(bar(kSFree), (i - 1) & 1)) && (t < w.t_end || mbar_test(bar(kQFull), seg & 1)))
+        r = 1;
+      else if (j < i && mbar_test(bar(kPFull), j & 1))
+        r = 2;
+      else if (global_timer_ns() - t0 > kWaitLimitNs || *fail)
+        r = 3;
+      r = __shfl_sync(kFullMask, r, 0);
+      if (r == 0) continue;
+      if (r == 3) {
+        ok = false;
+        break;
+      }
+      // Every lane has seen the phases that lane 0 saw (they are complete).
+      if (r == 1) {
+        const int st = i % kStages;
+        mbar_wait_bounded(bar(kKFull + st), (i / kStages) & 1);
+        if (t >= w.t_end) {
+          w.next(a);
+          t = w.t_begin;
+          firsts |= 1u << (i % 32);
+          ++seg;
+        } else {
+          firsts &= ~(1u << (i % 32));
         }
-        ok = ok && uni(mbar_wait_bounded(bar(2 + st), (g >> 1) & 1));
-        if (!ok) break;
         // Rows past the context: stale slots may hold anything, and 0 * NaN
         // would poison O (their logits are masked).
         const int live = w.c - t * kTile;
         if (live < kTile) {
-          unsigned char* v = sm + kOffK + st * kTileBytes;
+          unsigned char* v = sm + st * kStageBytes;
           const int chunks = (kTile - live) * 8;
-          for (int i = lane; i < chunks * kAtoms; i += 32) {
-            const int at = i / chunks, r = live + (i % chunks) / 8, ch = i % 8;
-            *reinterpret_cast<uint4*>(v + at * kAtomBytes + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+          for (int q = lane; q < chunks * kAtoms; q += 32) {
+            const int at = q / chunks, rr = live + (q % chunks) / 8, ch = q % 8;
+            *reinterpret_cast<uint4*>(v + at * kAtomBytes + rr * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
         }
         tc_fence_after();
-        const uint64_t kd = k_desc + st * kStageStep;
+        const uint64_t kd = k_desc + st * kStep;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kLatentRow / 16; ++k) {
-          const uint64_t off = (uint64_t)(((k / 4) * kAtomBytes + (k % 4) * 32) >> 4);
-          umma_f16_if(leader, tmem + kColS + 64 * st, q_desc + off, kd + off, kIdQK, k > 0);
+          for (int k = 0; k < 16; ++k)
+            umma_f16_tmem_a(tmem + kColS, tmem + kColQ + 8 * k,
+                            kd + (uint64_t)(((k / 4) * kAtomBytes + (k % 4) * 32) >> 4), kIdQK, k > 0);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            umma_f16_tmem_a(tmem + kColS, tmem + kColQ + 128 + 8 * k,
+                            kd + (uint64_t)((4 * kAtomBytes + k * 32) >> 4) + (uint64_t)(rank * 4), kIdQK, true);
+          umma_commit(bar(kSFull));
         }
-        umma_commit_if(leader, bar(6 + st));
-        ++qk;
-        if (t + 1 == w.t_end) umma_commit_if(leader, bar(1));  // the queries' last reader
-        if (pv < g) {
-          ok = uni(mbar_wait_bounded(bar(8), (g - 1) & 1));
-          if (ok) pv_mma(g - 1, prev_first);
+        __syncwarp();
+        ++i;
+        ++t;
+      } else {
+        const int st = j % kStages;
+        const bool first = firsts >> (j % 32) & 1;
+        tc_fence_after();
+        const uint64_t vd = v_desc + st * kStep;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            umma_f16_tmem_a(tmem, tmem + kColP + 8 * k, vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV,
+                            !first || k > 0);
+          umma_commit(bar(kKEmpty + st));
+          umma_commit(bar(kOFull));
         }
-        prev_first = t == w.t_begin;
+        __syncwarp();
+        ++j;
       }
-      ++seg;
-    }
-    if (ok && g > 0) {
-      ok = uni(mbar_wait_bounded(bar(8), (g - 1) & 1));
-      if (ok) pv_mma(g - 1, prev_first);
+      t0 = global_timer_ns();
     }
     if (!ok && lane == 0) {
       atomicOr(a.err, PA_ERRBIT_TIMEOUT);
       *fail = 1;
       // Every product started ends (bounded) before its memory goes.
-      if (qk > 0) mbar_wait_bounded(bar(6 + ((qk - 1) & 1)), ((qk - 1) >> 1) & 1);
-      if (pv > 0) mbar_wait_bounded(bar(9), (pv - 1) & 1);
+      if (i > 0) mbar_wait_bounded(bar(kSFull), (i - 1) & 1);
+      if (j > 0) mbar_wait_bounded(bar(kOFull), (j - 1) & 1);
     }
   } else {
-    // ---------------- softmax: lane l < 16 of warp i owns head row 16 i + l;
-    // lanes 16-31 hold the upper output values of the same rows
+    // ---------------- softmax: one head row a thread
     const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
-    const int row = 16 * warp + (lane & 15);
-    const int h = h0 + row;
-    const bool live_warp = h0 + 16 * warp < a.num_heads;
-    unsigned char* p_row = sm + kOffP + row * 128;
-    int g = 0;
+    const int h = h0 + tid;
+    const bool live = warp < live_warps;
+    const uint32_t x_peer = peer_address(s_base + kOffX, rank ^ 1) + tid * 16;
+    const uint32_t x_full_peer = peer_address(bar(kXFull), rank ^ 1);
+    const uint32_t x_free_peer = peer_address(bar(kXFree), rank ^ 1);
+    const unsigned char* x_own = sm + kOffX + tid * 16;
+    const uint32_t x_bytes = (uint32_t)live_warps * 32 * kTile * 4;
+    auto all = [&](bool v) { return __all_sync(kFullMask, v && !*fail); };
+    if (tid == 0 && n_tiles > 0) {
+      mbar_arrive_expect_tx(bar(kXFull), x_bytes);
+      mbar_arrive_expect_tx(bar(kXFull + 1), x_bytes);
+    }
+    int g = 0;  // tile
     bool ok = true;
-    while (ok && w.next(a)) {
-      float m = -INFINITY, l = 0.f;
-      for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
-        const int st = g & 1;
-        ok = __all_sync(kFullMask, mbar_wait_bounded(bar(6 + st), (g >> 1) & 1) && !*fail);
-        if (!ok) break;
+    // Takes this CTA's half of S of tile n to registers and sends it.
+    auto take = [&](int n, uint32_t (&sr)[kTile]) {
+      if (!all(mbar_wait_bounded(bar(kSFull), n & 1))) return false;
+      if (live) {
         tc_fence_after();
+        tmem_ld32(tmem + t_lane + kColS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+        tmem_ld32(tmem + t_lane + kColS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+        tmem_wait_ld();
+        tc_fence_before();
+      }
+      mbar_arrive(bar(kSFree));
+      if (live) {
+        const int b = n & 1;
+        if (n >= 2 && !all(mbar_wait_cluster(bar(kXFree + b), ((n >> 1) - 1) & 1))) return false;
+#pragma unroll
+        for (int c = 0; c < kTile / 4; ++c)
+          send16(x_peer + b * kXBytes + c * (kRows * 16), x_full_peer + 8 * b, sr[4 * c], sr[4 * c + 1],
+                 sr[4 * c + 2], sr[4 * c + 3]);
+      }
+      return true;
+    };
+    while (ok && w.next(a)) {
+      // The queries to tensor memory (the last segment's Q K^T products are
+      // done: their S has been taken).  Rows past the heads are zero.
+      if (live) {
+        const __half* q = static_cast<const __half*>(a.query) +
+                          ((size_t)(a.seq_begin + w.cur) * a.num_heads + (h < a.num_heads ? h : 0)) * kLatentRow;
+#pragma unroll
+        for (int cb = 0; cb < 5; ++cb) {
+          const uint4* src = reinterpret_cast<const uint4*>(q + (cb < 4 ? rank * kHalf + cb * 64
+                                                                        : kLatentDim + rank * (kRopeDim / 2)));
+          uint32_t r[32];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 v = (cb < 4 || c < 4) && h < a.num_heads ? src[c] : make_uint4(0, 0, 0, 0);
+            r[4 * c] = v.x;
+            r[4 * c + 1] = v.y;
+            r[4 * c + 2] = v.z;
+            r[4 * c + 3] = v.w;
+          }
+          tmem_st32(tmem + t_lane + kColQ + 32 * cb, r);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      mbar_arrive(bar(kQFull));
+      float m = -INFINITY, l = 0.f;
+      uint32_t sr[kTile], nx[kTile];
+      ok = take(g, sr);
+      for (int t = w.t_begin; ok && t < w.t_end; ++t, ++g) {
+        if (t + 1 < w.t_end) {
+          ok = take(g + 1, nx);
+          if (!ok) break;
+        }
         uint32_t pk[kTile / 2];
         float alpha = 1.f;
-        if (live_warp) {
-          uint32_t sr[kTile];
-          tmem_ld32(tmem + t_lane + kColS + 64 * st, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-          tmem_ld32(tmem + t_lane + kColS + 64 * st + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-          tmem_wait_ld();
+        bool rescale = false;
+        const int b = g & 1;
+        if (live) {
+          // The other half.
+          ok = all(mbar_wait_cluster(bar(kXFull + b), (g >> 1) & 1));
+          if (!ok) break;
           float x[kTile];
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) x[j] = __uint_as_float(sr[j]) * a.scale_log2;
-          const int live = w.c - t * kTile;
-          if (live < kTile) {
+          for (int c = 0; c < kTile / 4; ++c) {
+            const float4 v = *reinterpret_cast<const float4*>(x_own + b * kXBytes + c * (kRows * 16));
+            x[4 * c] = (__uint_as_float(sr[4 * c]) + v.x) * a.scale_log2;
+            x[4 * c + 1] = (__uint_as_float(sr[4 * c + 1]) + v.y) * a.scale_log2;
+            x[4 * c + 2] = (__uint_as_float(sr[4 * c + 2]) + v.z) * a.scale_log2;
+            x[4 * c + 3] = (__uint_as_float(sr[4 * c + 3]) + v.w) * a.scale_log2;
+          }
+          const int left = w.c - t * kTile;
+          if (left < kTile) {
 #pragma unroll
-            for (int j = 0; j < kTile; ++j)
-              if (j >= live) x[j] = -INFINITY;
+            for (int c = 0; c < kTile; ++c)
+              if (c >= left) x[c] = -INFINITY;
           }
           float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < kTile; j += 8)
+          for (int c = 0; c < kTile; c += 8)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) mq[u] = fmax3(mq[u], x[j + 2 * u], x[j + 2 * u + 1]);
+            for (int u = 0; u < 4; ++u) mq[u] = fmax3(mq[u], x[c + 2 * u], x[c + 2 * u + 1]);
           const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
           if (mx > m + kRescale || m == -INFINITY) {
             alpha = m == -INFINITY ? 1.f : exp2_approx(m - mx);
             m = mx;
           }
+          rescale = __any_sync(kFullMask, alpha != 1.f);
+          // The vote needed every lane's values, so the buffer's loads have
+          // returned: it is armed for tile g + 2 and given back.  (A release at
+          // cluster scope would wait for the sends in flight as well: 0.9 us a
+          // tile.)
+          if (tid == 0 && g + 2 < n_tiles) mbar_arrive_expect_tx(bar(kXFull + b), x_bytes);
+          if (lane == 0) mbar_arrive_remote(x_free_peer + 8 * b);
           const float ref = m == -INFINITY ? 0.f : m;
           float sq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < kTile / 2; ++j) {
-            pk[j] = exp2_f32_to_f16x2(x[2 * j] - ref, x[2 * j + 1] - ref);
-            sq[j & 3] = add_f16x2_f32(pk[j], sq[j & 3]);
+          for (int c = 0; c < kTile / 2; ++c) {
+            pk[c] = exp2_f32_to_f16x2(x[2 * c] - ref, x[2 * c + 1] - ref);
+            sq[c & 3] = add_f16x2_f32(pk[c], sq[c & 3]);
           }
           l = l * alpha + ((sq[0] + sq[1]) + (sq[2] + sq[3]));
         }
         // P and O are free once P.V of the tile before is done (a segment's
         // epilogue has waited for its last).
         if (t > w.t_begin) {
-          ok = __all_sync(kFullMask, mbar_wait_bounded(bar(9), (g - 1) & 1) && !*fail);
+          ok = all(mbar_wait_bounded(bar(kOFull), (g - 1) & 1));
           if (!ok) break;
-          tc_fence_after();
         }
-        if (live_warp) {
-          // Lanes 16-31 saw no logits of their own: the row's factor comes
-          // from the lane that did.
-          const float al = __shfl_sync(kFullMask, alpha, lane & 15);
-          if (t > w.t_begin && __any_sync(kFullMask, al != 1.f)) {
+        if (live) {
+          tc_fence_after();
+          if (t > w.t_begin && rescale) {
 #pragma unroll
-            for (int cb = 0; cb < 8; ++cb) {
+            for (int cb = 0; cb < kHalf / 32; ++cb) {
               uint32_t r[32];
               tmem_ld32(tmem + t_lane + cb * 32, r);
               tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * al);
+              for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * alpha);
               tmem_st32(tmem + t_lane + cb * 32, r);
             }
-            tmem_wait_st();
           }
-          if (lane < 16) {
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch)
-              *reinterpret_cast<uint4*>(p_row + ((ch ^ (row & 7)) << 4)) =
-                  make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
-          }
-          fence_proxy_async_smem();
+          tmem_st32(tmem + t_lane + kColP, pk);
+          tmem_wait_st();
+          tc_fence_before();
         }
-        tc_fence_before();
-        mbar_arrive(bar(8));
+        mbar_arrive(bar(kPFull));
+#pragma unroll
+        for (int c = 0; c < kTile; ++c) sr[c] = nx[c];
       }
       if (!ok) break;
       // The segment's output: to `out` when it is the whole sequence, else a
       // partial.
-      ok = __all_sync(kFullMask, mbar_wait_bounded(bar(9), (g - 1) & 1) && !*fail);
+      ok = all(mbar_wait_bounded(bar(kOFull), (g - 1) & 1));
       if (!ok) break;
-      tc_fence_after();
-      if (live_warp) {
-        const float lr = __shfl_sync(kFullMask, l, lane & 15);
-        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+      if (live) {
+        tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : 0.f;
         const bool whole = w.t_begin == 0 && w.t_end == w.n;
         const size_t sh = (size_t)(a.seq_begin + w.cur) * a.num_heads + h;
         const size_t ph = (size_t)(w.cur + worker) * a.num_heads + h;
-        if (!whole && lane < 16 && h < a.num_heads) a.ws_ml[ph] = make_float2(m, l);
-        const int d0 = lane < 16 ? 0 : 256;
-        __half* orow = static_cast<__half*>(a.out) + sh * kLatentDim + d0;
-        float* prow = a.ws_o + ph * kLatentDim + d0;
+        if (!whole && rank == 0 && h < a.num_heads) a.ws_ml[ph] = make_float2(m, l);
+        __half* orow = static_cast<__half*>(a.out) + sh * kLatentDim + rank * kHalf;
+        float* prow = a.ws_o + ph * kLatentDim + rank * kHalf;
 #pragma unroll
-        for (int cb = 0; cb < 8; ++cb) {
+        for (int cb = 0; cb < kHalf / 32; ++cb) {
           uint32_t r[32];
           tmem_ld32(tmem + t_lane + cb * 32, r);
           tmem_wait_ld();
@@ -530,24 +647,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<uint4*>(prow + cb * 32 + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+              for (int c = 0; c < 32; c += 4)
+                *reinterpret_cast<uint4*>(prow + cb * 32 + c) = make_uint4(r[c], r[c + 1], r[c + 2], r[c + 3]);
             }
           }
         }
+        tc_fence_before();
       }
-      tc_fence_before();
     }
     if (!ok && lane == 0) *fail = 1;
   }
   tc_fence_before();
-  mbar_arrive(bar(10));
+  mbar_arrive(bar(kDone));
   if (warp == 4) {
-    if (!mbar_wait_bounded(bar(10), 0) && lane == 0) atomicOr(a.err, PA_ERRBIT_TIMEOUT);
+    if (!mbar_wait_bounded(bar(kDone), 0) && lane == 0) atomicOr(a.err, PA_ERRBIT_TIMEOUT);
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  __syncwarp();
+  cluster_sync();  // nothing of the other CTA is on its way to this one's memory
 }
 
 // Joins the segments of each (sequence, head): with M = max m_i,
@@ -598,7 +717,7 @@ struct LatentLayout {
 LatentLayout latent_layout(int num_seqs, int num_heads, int sms) {
   LatentLayout l{};
   l.head_tiles = (num_heads + kRows - 1) / kRows;
-  l.workers = sms / l.head_tiles > 0 ? sms / l.head_tiles : 1;
+  l.workers = sms / 2 / l.head_tiles > 0 ? sms / 2 / l.head_tiles : 1;
   const int seqs = num_seqs < kSeqsPerLaunch ? num_seqs : kSeqsPerLaunch;
   const size_t slots = (size_t)seqs + l.workers;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
@@ -641,16 +760,14 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
   }
   const LatentLayout l = latent_layout(g.num_seqs, g.num_heads, g.sms);
   const long long rows = (long long)g.num_blocks * g.block_size;
-  CUtensorMap tq, tc;
+  CUtensorMap tc;
   const cuuint64_t str[1] = {(cuuint64_t)kLatentRow * 2};
-  const cuuint64_t qdims[2] = {(cuuint64_t)kLatentRow, (cuuint64_t)g.num_seqs * g.num_heads};
   const cuuint64_t cdims[2] = {(cuuint64_t)kLatentRow, (cuuint64_t)rows};
-  const cuuint32_t qbox[2] = {64, (cuuint32_t)kRows}, cbox[2] = {64, (cuuint32_t)g.block_size};
-  if (!encode_tensor_map(&tq, g.query, 2, qdims, str, qbox) ||
-      !encode_tensor_map(&tc, g.cache, 2, cdims, str, cbox))
-    return cudaErrorInvalidValue;
+  const cuuint32_t cbox[2] = {64, (cuuint32_t)g.block_size};
+  if (!encode_tensor_map(&tc, g.cache, 2, cdims, str, cbox)) return cudaErrorInvalidValue;
   LatentParams p{};
   p.out = g.out;
+  p.query = g.query;
   p.block_tables = g.block_tables;
   p.context_lens = g.context_lens;
   p.cum = reinterpret_cast<int*>(g.workspace + l.cum);
@@ -669,8 +786,8 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
   for (int b = 0; b < g.num_seqs; b += kSeqsPerLaunch) {
     p.seq_begin = b;
     p.num_seqs = g.num_seqs - b < kSeqsPerLaunch ? g.num_seqs - b : kSeqsPerLaunch;
-    e = launch_pdl(latent_decode_kernel, dim3((unsigned)(l.workers * l.head_tiles)), dim3(kThreads),
-                   kSmem, stream, tq, tc, p);
+    e = launch_pdl_cluster(latent_decode_kernel, dim3((unsigned)(2 * l.workers * l.head_tiles)),
+                           dim3(kThreads), 2, kSmem, stream, tc, p);
     if (e != cudaSuccess) return e;
     e = launch_pdl(latent_merge_kernel, dim3((unsigned)((long long)p.num_seqs * p.num_heads)),
                    dim3(128), 0, stream, p);

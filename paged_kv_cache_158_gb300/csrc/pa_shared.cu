@@ -415,7 +415,6 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
     // ---------------- MMA
     constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
     constexpr uint32_t kIdPV = umma_idesc_f16(kRows, D, false, true);
-    const bool leader = lane == 0;
     const uint64_t q_desc = umma_desc_sw128(s_base, 16, 1024);
     const uint64_t k_desc = umma_desc_sw128(s_base + T::OFF_K, 16, 1024);
     const uint64_t v_desc = umma_desc_sw128(s_base + T::OFF_V, T::ATOM, 1024);
@@ -429,12 +428,15 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
       if (!ok) return false;
       tc_fence_after();
       const uint64_t vd = v_desc + (g % NST) * kStep;
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        umma_f16_tmem_a_if(leader, tmem + T::COL_O, tmem + 128 * (g & 1) + 8 * k,
-                           vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV, !first || k > 0);
-      umma_commit_if(leader, bar(kVEmpty + g % NST));
-      umma_commit_if(leader, bar(kOFull));
+        for (int k = 0; k < kTile / 16; ++k)
+          umma_f16_tmem_a(tmem + T::COL_O, tmem + 128 * (g & 1) + 8 * k,
+                          vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV, !first || k > 0);
+        umma_commit(bar(kVEmpty + g % NST));
+        umma_commit(bar(kOFull));
+      }
+      __syncwarp();
       ++pv;
       return true;
     };
@@ -451,15 +453,18 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const uint64_t kd = k_desc + st * kStep;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = (uint64_t)(((k / 4) * T::ATOM + (k % 4) * 32) >> 4);
-          umma_f16_if(leader, tmem + 128 * (g & 1), q_desc + off, kd + off, kIdQK, k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (uint64_t)(((k / 4) * T::ATOM + (k % 4) * 32) >> 4);
+            umma_f16(tmem + 128 * (g & 1), q_desc + off, kd + off, kIdQK, k > 0);
+          }
+          umma_commit(bar(kSFull + (g & 1)));
+          umma_commit(bar(kKEmpty + st));
+          if (t + 1 == w.t_end) umma_commit(bar(kQEmpty));  // the queries' last reader
         }
-        umma_commit_if(leader, bar(kSFull + (g & 1)));
-        umma_commit_if(leader, bar(kKEmpty + st));
+        __syncwarp();
         ++qk;
-        if (t + 1 == w.t_end) umma_commit_if(leader, bar(kQEmpty));  // the queries' last reader
         if (pv < g) ok = pv_mma(g - 1, prev_first);
         prev_first = t == w.t_begin;
       }
