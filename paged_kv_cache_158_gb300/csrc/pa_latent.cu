@@ -42,11 +42,13 @@
 //    (five 64-value swizzle atoms), copied by TMA one box a block and atom; it
 //    is the K operand of Q K^T and, its first four atoms read the other way
 //    round, the V operand of P V.
-//  * Four softmax warps (one head row a thread) send their half of S(t + 1)
-//    before they work on S(t), so the exchange overlaps the softmax.  Running
-//    reference and sum are fp32, P is rounded once to fp16 (the sum adds the
-//    rounded weights).  The reference moves only when the tile's maximum is
-//    more than 2^8 above it, so the output is seldom rescaled.
+//  * Two softmax warpgroups (one head row a thread) take alternate tiles, so
+//    one's exchange overlaps the other's exponentials.  The row's reference
+//    goes from tile to tile through shared memory; each group keeps the sum of
+//    its own tiles, joined at the segment's end.  References and sums are
+//    fp32, P is rounded once to fp16 (the sum adds the rounded weights).  The
+//    reference moves only when the tile's maximum is more than 2^8 above it,
+//    so the output is seldom rescaled.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -99,13 +101,16 @@ constexpr int kAtoms = 5;              // its 64-value atoms: four latent, the r
 constexpr int kAtomBytes = kTile * 128;
 constexpr int kStageBytes = kAtoms * kAtomBytes;
 constexpr int kStages = 4;
-constexpr int kThreads = 192;          // four softmax warps, TMA, MMA
+constexpr int kThreads = 320;          // two softmax warpgroups, TMA, MMA
+constexpr int kWarpTma = 8, kWarpMma = 9;
 constexpr int kSeqsPerLaunch = 1024;
 
 constexpr int kXBytes = kRows * kTile * 4;                 // one half of S from the other CTA
 constexpr int kOffX = kStages * kStageBytes;               // buffer b at kOffX + b * kXBytes
 constexpr int kOffBar = kOffX + 2 * kXBytes;
-constexpr int kSmem = kOffBar + 256 + 1024;                // + alignment slack
+constexpr int kOffRef = kOffBar + 256;                     // float [128]: each row's reference
+constexpr int kOffMl = kOffRef + kRows * 4;                // float2 [2][128]: reference and sum of each group
+constexpr int kSmem = kOffMl + 2 * kRows * 8;
 static_assert(kSmem <= 232448, "beyond the opt-in shared memory of one CTA");
 
 constexpr uint32_t kTmemCols = 512;    // O: [0, 256)
@@ -115,10 +120,12 @@ constexpr uint32_t kColP = 480;        // 32
 
 constexpr float kRescale = 8.f;        // base-2 logits above the reference that move it
 
-// Barriers.
+// Barriers.  Those of two phases at a time that one warpgroup sees every
+// other one of come in pairs, by the tile's parity.
 enum {
-  kKFull = 0, kKEmpty = 4, kQFull = 8, kSFull = 9, kSFree = 10, kPFull = 11, kOFull = 12, kXFull = 13 /* 2 */,
-  kXFree = 15 /* 2 */, kDone = 17, kNumBars = 18
+  kKFull = 0 /* 4 */, kKEmpty = 4 /* 4 */, kQFull = 8, kSFull = 9 /* 2 */, kSFree = 11, kPFull = 12,
+  kOFull = 13 /* 2 */, kXFull = 15 /* 2 */, kXFree = 17 /* 2 */, kRef = 19 /* 2 */, kSegA = 21, kSegB = 22, kDone = 23,
+  kNumBars = 24
 };
 
 struct LatentParams {
@@ -247,9 +254,7 @@ __device__ __forceinline__ void cluster_sync() {
 
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap tc, const LatentParams a) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) unsigned char sm[];  // the swizzle's phase is the address's
   const uint32_t s_base = smem_u32(sm);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -263,17 +268,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int worker = cluster / a.head_tiles, ht = cluster % a.head_tiles;
   const int h0 = ht * kRows;
   const int live_warps = min(4, (a.num_heads - h0 + 31) / 32);  // softmax warps with heads
-  if (tid == 160) {
+  if (tid == kWarpMma * 32) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i == kQFull || i == kSFree || i == kPFull ? 128
-                        : i == kXFree || i == kXFree + 1          ? live_warps
-                        : i == kDone                              ? kThreads
-                                                                  : 1);
+      mbar_init(bar(i), i == kSFree || i == kPFull || i == kRef || i == kRef + 1 ? 128
+                        : i == kQFull || i == kSegA || i == kSegB                 ? 256
+                        : i == kXFree || i == kXFree + 1                          ? live_warps
+                        : i == kDone                                              ? kThreads
+                                                                                  : 1);
     *fail = 0;
     fence_mbar_init();
     prefetch_tensormap(&tc);
   }
-  if (warp == 4) {
+  if (warp == kWarpTma) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   w.left = start[2];
   const int n_tiles = w.left;
 
-  if (warp == 4) {
+  if (warp == kWarpTma) {
     // ---------------- TMA: the tiles of the range
     const int nb = kTile / a.block_size;
     const int b = lane % nb;
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = max(0, g - kStages); u < g; ++u)
         mbar_wait_bounded(bar(kKFull + u % kStages), (u / kStages) & 1);
     }
-  } else if (warp == 5) {
+  } else if (warp == kWarpMma) {
     // ---------------- MMA: S of tile i and P.V of tile j, whichever can start.
     // S has one buffer (the softmax takes it to registers), P another.
     constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
@@ -384,15 +390,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.t_end = 0;
     bool ok = true;
     uint64_t t0 = global_timer_ns();
+    unsigned polls = 0;
     while (j < n_tiles) {
-      // 1: S(i) can start; 2: P.V(j) can.
+      // 2: P.V(j) can start; 1: S(i) can.  P.V first: the next tile's P waits
+      // for it.
       int r = 0;
-      if (i < n_tiles && mbar_test(bar(kKFull + i % kStages), (i / kStages) & 1) &&
-          (i == 0 || mbar_test(bar(kSFree), (i - 1) & 1)) && (t < w.t_end || mbar_test(bar(kQFull), seg & 1)))
-        r = 1;
-      else if (j < i && mbar_test(bar(kPFull), j & 1))
+      if (j < i && mbar_test(bar(kPFull), j & 1))
         r = 2;
-      else if (global_timer_ns() - t0 > kWaitLimitNs || *fail)
+      else if (i < n_tiles && (i == 0 || mbar_test(bar(kSFree), (i - 1) & 1)) &&
+               mbar_test(bar(kKFull + i % kStages), (i / kStages) & 1) &&
+               (t < w.t_end || mbar_test(bar(kQFull), seg & 1)))
+        r = 1;
+      else if ((++polls & 255) == 0 && (global_timer_ns() - t0 > kWaitLimitNs || *fail))
         r = 3;
       r = __shfl_sync(kFullMask, r, 0);
       if (r == 0) continue;
@@ -436,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 2; ++k)
             umma_f16_tmem_a(tmem + kColS, tmem + kColQ + 128 + 8 * k,
                             kd + (uint64_t)((4 * kAtomBytes + k * 32) >> 4) + (uint64_t)(rank * 4), kIdQK, true);
-          umma_commit(bar(kSFull));
+          umma_commit(bar(kSFull + (i & 1)));
         }
         __syncwarp();
         ++i;
@@ -452,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_f16_tmem_a(tmem, tmem + kColP + 8 * k, vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV,
                             !first || k > 0);
           umma_commit(bar(kKEmpty + st));
-          umma_commit(bar(kOFull));
+          umma_commit(bar(kOFull + (j & 1)));
         }
         __syncwarp();
         ++j;
@@ -463,65 +472,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       atomicOr(a.err, PA_ERRBIT_TIMEOUT);
       *fail = 1;
       // Every product started ends (bounded) before its memory goes.
-      if (i > 0) mbar_wait_bounded(bar(kSFull), (i - 1) & 1);
-      if (j > 0) mbar_wait_bounded(bar(kOFull), (j - 1) & 1);
+      if (i > 0) mbar_wait_bounded(bar(kSFull + ((i - 1) & 1)), ((i - 1) >> 1) & 1);
+      if (j > 0) mbar_wait_bounded(bar(kOFull + ((j - 1) & 1)), ((j - 1) >> 1) & 1);
     }
   } else {
-    // ---------------- softmax: one head row a thread
-    const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
-    const int h = h0 + tid;
-    const bool live = warp < live_warps;
-    const uint32_t x_peer = peer_address(s_base + kOffX, rank ^ 1) + tid * 16;
-    const uint32_t x_full_peer = peer_address(bar(kXFull), rank ^ 1);
-    const uint32_t x_free_peer = peer_address(bar(kXFree), rank ^ 1);
-    const unsigned char* x_own = sm + kOffX + tid * 16;
+    // ---------------- softmax: one head row a thread; warpgroup x takes the
+    // tiles g = x mod 2
+    const int x = warp >> 2, row = tid & 127;
+    const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
+    const int h = h0 + row;
+    const bool live = (warp & 3) < live_warps;
+    const uint32_t x_peer = peer_address(s_base + kOffX + x * kXBytes, rank ^ 1) + row * 16;
+    const uint32_t x_full_peer = peer_address(bar(kXFull + x), rank ^ 1);
+    const uint32_t x_free_peer = peer_address(bar(kXFree + x), rank ^ 1);
+    const unsigned char* x_own = sm + kOffX + x * kXBytes + row * 16;
     const uint32_t x_bytes = (uint32_t)live_warps * 32 * kTile * 4;
+    float* ref_s = reinterpret_cast<float*>(sm + kOffRef) + row;
+    float2* ml_s = reinterpret_cast<float2*>(sm + kOffMl) + row;
     auto all = [&](bool v) { return __all_sync(kFullMask, v && !*fail); };
-    if (tid == 0 && n_tiles > 0) {
-      mbar_arrive_expect_tx(bar(kXFull), x_bytes);
-      mbar_arrive_expect_tx(bar(kXFull + 1), x_bytes);
-    }
-    int g = 0;  // tile
+    if (row == 0 && x < n_tiles) mbar_arrive_expect_tx(bar(kXFull + x), x_bytes);
+    // A negative multiplier's sign goes into the queries: the largest product
+    // is then the largest logit.
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const float scale = fabsf(a.scale_log2);
+    const uint64_t scale2 = f32x2_splat(scale);
+    int g = 0, seg = 0;
     bool ok = true;
-    // Takes this CTA's half of S of tile n to registers and sends it.
-    auto take = [&](int n, uint32_t (&sr)[kTile]) {
-      if (!all(mbar_wait_bounded(bar(kSFull), n & 1))) return false;
-      if (live) {
-        tc_fence_after();
-        tmem_ld32(tmem + t_lane + kColS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-        tmem_ld32(tmem + t_lane + kColS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-        tmem_wait_ld();
-        tc_fence_before();
-      }
-      mbar_arrive(bar(kSFree));
-      if (live) {
-        const int b = n & 1;
-        if (n >= 2 && !all(mbar_wait_cluster(bar(kXFree + b), ((n >> 1) - 1) & 1))) return false;
-#pragma unroll
-        for (int c = 0; c < kTile / 4; ++c)
-          send16(x_peer + b * kXBytes + c * (kRows * 16), x_full_peer + 8 * b, sr[4 * c], sr[4 * c + 1],
-                 sr[4 * c + 2], sr[4 * c + 3]);
-      }
-      return true;
-    };
     while (ok && w.next(a)) {
-      // The queries to tensor memory (the last segment's Q K^T products are
-      // done: their S has been taken).  Rows past the heads are zero.
+      // The queries to tensor memory, half of them by each group (the last
+      // segment's Q K^T products are done: their S has been taken).  Rows past
+      // the heads are zero.
       if (live) {
         const __half* q = static_cast<const __half*>(a.query) +
                           ((size_t)(a.seq_begin + w.cur) * a.num_heads + (h < a.num_heads ? h : 0)) * kLatentRow;
 #pragma unroll
-        for (int cb = 0; cb < 5; ++cb) {
+        for (int k = 0; k < 3; ++k) {
+          const int cb = x == 0 ? k : 3 + k;  // group 0: columns 0-95; group 1: 96-127 and the rotary 16
+          if (cb > 4) break;
           const uint4* src = reinterpret_cast<const uint4*>(q + (cb < 4 ? rank * kHalf + cb * 64
                                                                         : kLatentDim + rank * (kRopeDim / 2)));
           uint32_t r[32];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const uint4 v = (cb < 4 || c < 4) && h < a.num_heads ? src[c] : make_uint4(0, 0, 0, 0);
-            r[4 * c] = v.x;
-            r[4 * c + 1] = v.y;
-            r[4 * c + 2] = v.z;
-            r[4 * c + 3] = v.w;
+            r[4 * c] = v.x ^ flip;
+            r[4 * c + 1] = v.y ^ flip;
+            r[4 * c + 2] = v.z ^ flip;
+            r[4 * c + 3] = v.w ^ flip;
           }
           tmem_st32(tmem + t_lane + kColQ + 32 * cb, r);
         }
@@ -529,73 +526,101 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
       }
       mbar_arrive(bar(kQFull));
-      float m = -INFINITY, l = 0.f;
-      uint32_t sr[kTile], nx[kTile];
-      ok = take(g, sr);
-      for (int t = w.t_begin; ok && t < w.t_end; ++t, ++g) {
-        if (t + 1 < w.t_end) {
-          ok = take(g + 1, nx);
-          if (!ok) break;
+      const int g_end = g + w.t_end - w.t_begin;
+      float m = -INFINITY, l = 0.f;  // this group's reference and sum
+      for (int t = w.t_begin; g < g_end; ++t, ++g) {
+        if ((g & 1) != x) continue;
+        const uint32_t par = (g >> 1) & 1;
+        const bool first = t == w.t_begin;
+        ok = all(mbar_wait_bounded(bar(kSFull + x), par));
+        if (!ok) break;
+        uint32_t sr[kTile];
+        if (live) {
+          tc_fence_after();
+          tmem_ld32(tmem + t_lane + kColS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+          tmem_ld32(tmem + t_lane + kColS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+          tmem_wait_ld();
+          tc_fence_before();
         }
+        mbar_arrive(bar(kSFree));
         uint32_t pk[kTile / 2];
         float alpha = 1.f;
         bool rescale = false;
-        const int b = g & 1;
         if (live) {
-          // The other half.
-          ok = all(mbar_wait_cluster(bar(kXFull + b), (g >> 1) & 1));
+          // This CTA's half of the logits to the other one; the other's half.
+          ok = g < 2 || all(mbar_wait_cluster(bar(kXFree + x), par ^ 1));
           if (!ok) break;
-          float x[kTile];
+#pragma unroll
+          for (int c = 0; c < kTile / 4; ++c)
+            send16(x_peer + c * (kRows * 16), x_full_peer, sr[4 * c], sr[4 * c + 1], sr[4 * c + 2], sr[4 * c + 3]);
+          ok = all(mbar_wait_cluster(bar(kXFull + x), par));
+          if (!ok) break;
+          float y[kTile];
 #pragma unroll
           for (int c = 0; c < kTile / 4; ++c) {
-            const float4 v = *reinterpret_cast<const float4*>(x_own + b * kXBytes + c * (kRows * 16));
-            x[4 * c] = (__uint_as_float(sr[4 * c]) + v.x) * a.scale_log2;
-            x[4 * c + 1] = (__uint_as_float(sr[4 * c + 1]) + v.y) * a.scale_log2;
-            x[4 * c + 2] = (__uint_as_float(sr[4 * c + 2]) + v.z) * a.scale_log2;
-            x[4 * c + 3] = (__uint_as_float(sr[4 * c + 3]) + v.w) * a.scale_log2;
+            const float4 v = *reinterpret_cast<const float4*>(x_own + c * (kRows * 16));
+            y[4 * c] = __uint_as_float(sr[4 * c]) + v.x;
+            y[4 * c + 1] = __uint_as_float(sr[4 * c + 1]) + v.y;
+            y[4 * c + 2] = __uint_as_float(sr[4 * c + 2]) + v.z;
+            y[4 * c + 3] = __uint_as_float(sr[4 * c + 3]) + v.w;
           }
           const int left = w.c - t * kTile;
           if (left < kTile) {
 #pragma unroll
             for (int c = 0; c < kTile; ++c)
-              if (c >= left) x[c] = -INFINITY;
+              if (c >= left) y[c] = -INFINITY;
           }
           float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int c = 0; c < kTile; c += 8)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) mq[u] = fmax3(mq[u], x[c + 2 * u], x[c + 2 * u + 1]);
-          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-          if (mx > m + kRescale || m == -INFINITY) {
-            alpha = m == -INFINITY ? 1.f : exp2_approx(m - mx);
-            m = mx;
+            for (int u = 0; u < 4; ++u) mq[u] = fmax3(mq[u], y[c + 2 * u], y[c + 2 * u + 1]);
+          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * scale;
+          // The reference after the tile before.
+          float before = -INFINITY;
+          if (!first) {
+            ok = all(mbar_wait_bounded(bar(kRef + (x ^ 1)), ((g - 1) >> 1) & 1));
+            if (!ok) break;
+            before = *ref_s;
           }
+          const float ref = mx > before + kRescale || before == -INFINITY ? mx : before;
+          *ref_s = ref;
+          mbar_arrive(bar(kRef + x));
+          alpha = before == -INFINITY || ref == before ? 1.f : exp2_approx(before - ref);
           rescale = __any_sync(kFullMask, alpha != 1.f);
           // The vote needed every lane's values, so the buffer's loads have
           // returned: it is armed for tile g + 2 and given back.  (A release at
           // cluster scope would wait for the sends in flight as well: 0.9 us a
           // tile.)
-          if (tid == 0 && g + 2 < n_tiles) mbar_arrive_expect_tx(bar(kXFull + b), x_bytes);
-          if (lane == 0) mbar_arrive_remote(x_free_peer + 8 * b);
-          const float ref = m == -INFINITY ? 0.f : m;
+          if (row == 0 && g + 2 < n_tiles) mbar_arrive_expect_tx(bar(kXFull + x), x_bytes);
+          if (lane == 0) mbar_arrive_remote(x_free_peer);
+          const uint64_t neg2 = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
           float sq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < kTile / 2; ++c) {
-            pk[c] = exp2_f32_to_f16x2(x[2 * c] - ref, x[2 * c + 1] - ref);
+            const float2 e = ffma2(y[2 * c], y[2 * c + 1], scale2, neg2);
+            pk[c] = exp2_f32_to_f16x2(e.x, e.y);
             sq[c & 3] = add_f16x2_f32(pk[c], sq[c & 3]);
           }
-          l = l * alpha + ((sq[0] + sq[1]) + (sq[2] + sq[3]));
+          l = l * (m == -INFINITY || ref == m ? 1.f : exp2_approx(m - ref)) + ((sq[0] + sq[1]) + (sq[2] + sq[3]));
+          m = ref;
+        } else {
+          if (!first) {
+            ok = all(mbar_wait_bounded(bar(kRef + (x ^ 1)), ((g - 1) >> 1) & 1));
+            if (!ok) break;
+          }
+          mbar_arrive(bar(kRef + x));
         }
         // P and O are free once P.V of the tile before is done (a segment's
         // epilogue has waited for its last).
-        if (t > w.t_begin) {
-          ok = all(mbar_wait_bounded(bar(kOFull), (g - 1) & 1));
+        if (!first) {
+          ok = all(mbar_wait_bounded(bar(kOFull + (x ^ 1)), ((g - 1) >> 1) & 1));
           if (!ok) break;
         }
         if (live) {
           tc_fence_after();
-          if (t > w.t_begin && rescale) {
-#pragma unroll
+          if (!first && rescale) {
+#pragma unroll 1  // seldom taken: unrolled, it costs the loop its registers
             for (int cb = 0; cb < kHalf / 32; ++cb) {
               uint32_t r[32];
               tmem_ld32(tmem + t_lane + cb * 32, r);
@@ -610,27 +635,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
         }
         mbar_arrive(bar(kPFull));
-#pragma unroll
-        for (int c = 0; c < kTile; ++c) sr[c] = nx[c];
       }
       if (!ok) break;
-      // The segment's output: to `out` when it is the whole sequence, else a
-      // partial.
-      ok = all(mbar_wait_bounded(bar(kOFull), (g - 1) & 1));
+      g = g_end;
+      // The groups' references and sums, joined at the last reference.
+      ml_s[x * kRows] = make_float2(m, l);
+      mbar_arrive(bar(kSegA));
+      ok = all(mbar_wait_bounded(bar(kSegA), seg & 1));
       if (!ok) break;
+      const int last = g - 1;
+      ok = all(mbar_wait_bounded(bar(kOFull + (last & 1)), (last >> 1) & 1));
+      if (!ok) break;
+      // The segment's output, half of it by each group: to `out` when it is the
+      // whole sequence, else a partial.
       if (live) {
         tc_fence_after();
+        const float2 me = ml_s[(last & 1) * kRows], other = ml_s[((last & 1) ^ 1) * kRows];
+        m = me.x;
+        l = me.y + (other.x == -INFINITY ? 0.f : other.y * exp2_approx(other.x - m));
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const bool whole = w.t_begin == 0 && w.t_end == w.n;
         const size_t sh = (size_t)(a.seq_begin + w.cur) * a.num_heads + h;
         const size_t ph = (size_t)(w.cur + worker) * a.num_heads + h;
-        if (!whole && rank == 0 && h < a.num_heads) a.ws_ml[ph] = make_float2(m, l);
-        __half* orow = static_cast<__half*>(a.out) + sh * kLatentDim + rank * kHalf;
-        float* prow = a.ws_o + ph * kLatentDim + rank * kHalf;
-#pragma unroll
-        for (int cb = 0; cb < kHalf / 32; ++cb) {
+        if (!whole && rank == 0 && x == 0 && h < a.num_heads) a.ws_ml[ph] = make_float2(m, l);
+        const int d0 = rank * kHalf + x * (kHalf / 2);
+        __half* orow = static_cast<__half*>(a.out) + sh * kLatentDim + d0;
+        float* prow = a.ws_o + ph * kLatentDim + d0;
+#pragma unroll 1
+        for (int cb = 0; cb < kHalf / 64; ++cb) {
           uint32_t r[32];
-          tmem_ld32(tmem + t_lane + cb * 32, r);
+          tmem_ld32(tmem + t_lane + x * (kHalf / 2) + cb * 32, r);
           tmem_wait_ld();
           if (h < a.num_heads) {
             if (whole) {
@@ -654,12 +688,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
       }
+      // Both groups have read O and the sums before the next segment's are written.
+      mbar_arrive(bar(kSegB));
+      ok = all(mbar_wait_bounded(bar(kSegB), seg & 1));
+      ++seg;
     }
     if (!ok && lane == 0) *fail = 1;
   }
   tc_fence_before();
   mbar_arrive(bar(kDone));
-  if (warp == 4) {
+  if (warp == kWarpTma) {
     if (!mbar_wait_bounded(bar(kDone), 0) && lane == 0) atomicOr(a.err, PA_ERRBIT_TIMEOUT);
     __syncwarp();
     tc_fence_after();
@@ -671,40 +709,87 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the segments of each (sequence, head): with M = max m_i,
 //   out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
-// 128 threads, four values each; a sequence of no tokens gets zeros, one that
-// a single worker covered is already written.
-__global__ void __launch_bounds__(128) latent_merge_kernel(const LatentParams a) {
+// One CTA a pair; 128 threads, four values each, take the segments in turn with
+// the other groups of 128 (few pairs with many segments need several; the
+// order of the sums goes by the batch's shape alone).  A sequence of no tokens
+// gets zeros, one that a single worker covered is already written.
+constexpr int kMergeGroups = 4;
+constexpr int kMergeChunk = 128;  // segments whose weights are held at a time
+
+__global__ void __launch_bounds__(128 * kMergeGroups) latent_merge_kernel(const LatentParams a) {
+  __shared__ float wt_s[kMergeChunk];
+  __shared__ float red[16];
+  __shared__ float4 part[kMergeGroups - 1][128];
   pdl_wait();
   pdl_launch_dependents();
+  const int tid = threadIdx.x, group = tid >> 7, groups = (int)blockDim.x >> 7, d4 = tid & 127;
+  const int warp = tid >> 5, lane = tid & 31, warps = (int)blockDim.x >> 5;
   const int s = (int)blockIdx.x / a.num_heads, h = (int)blockIdx.x - s * a.num_heads;
   const int c0 = a.cum[s], c1 = a.cum[s + 1], total = a.cum[a.num_seqs];
   __half* out = static_cast<__half*>(a.out) +
-                ((size_t)(a.seq_begin + s) * a.num_heads + h) * kLatentDim + 4 * threadIdx.x;
+                ((size_t)(a.seq_begin + s) * a.num_heads + h) * kLatentDim + 4 * d4;
   if (c0 == c1) {
-    *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
+    if (group == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
     return;
   }
   const int W = active_workers(a, total);
   const int w0 = worker_of(c0, W, total), w1 = worker_of(c1 - 1, W, total);
   if (w0 == w1) return;
+  const int n = w1 - w0 + 1;
   const size_t base = (size_t)(s + w0) * a.num_heads + h;
+  auto block_max = [&](float v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    for (int i = 0; i < warps; ++i) v = fmaxf(v, red[i]);
+    __syncthreads();
+    return v;
+  };
   float M = -INFINITY;
-  for (int i = 0; i <= w1 - w0; ++i) M = fmaxf(M, a.ws_ml[base + (size_t)i * a.num_heads].x);
-  float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int i = 0; i <= w1 - w0; ++i) {
-    const size_t at = base + (size_t)i * a.num_heads;
-    const float2 ml = a.ws_ml[at];
-    const float4 v = *reinterpret_cast<const float4*>(a.ws_o + at * kLatentDim + 4 * threadIdx.x);
-    const float wt = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - M);
-    L = fmaf(wt, ml.y, L);
-    o[0] = fmaf(wt, v.x, o[0]);
-    o[1] = fmaf(wt, v.y, o[1]);
-    o[2] = fmaf(wt, v.z, o[2]);
-    o[3] = fmaf(wt, v.w, o[3]);
+  for (int i = tid; i < n; i += (int)blockDim.x) M = fmaxf(M, a.ws_ml[base + (size_t)i * a.num_heads].x);
+  M = block_max(M);
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += kMergeChunk) {
+    const int cnt = min(kMergeChunk, n - i0);
+    if (tid < cnt) {
+      const float2 ml = a.ws_ml[base + (size_t)(i0 + tid) * a.num_heads];
+      const float wt = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - M);
+      wt_s[tid] = wt;
+      L = fmaf(wt, ml.y, L);
+    }
+    __syncthreads();
+    const float* src = a.ws_o + (base + (size_t)i0 * a.num_heads) * kLatentDim + 4 * d4;
+    const size_t step = (size_t)a.num_heads * kLatentDim;
+#pragma unroll 8
+    for (int i = group; i < cnt; i += groups) {
+      const float4 v = *reinterpret_cast<const float4*>(src + i * step);
+      const float x = wt_s[i];
+      o.x = fmaf(x, v.x, o.x);
+      o.y = fmaf(x, v.y, o.y);
+      o.z = fmaf(x, v.z, o.z);
+      o.w = fmaf(x, v.w, o.w);
+    }
+    __syncthreads();
+  }
+  if (group > 0) part[group - 1][d4] = o;
+#pragma unroll
+  for (int k = 16; k >= 1; k >>= 1) L += __shfl_xor_sync(kFullMask, L, k);
+  if (lane == 0) red[warp] = L;
+  __syncthreads();
+  if (group > 0) return;
+  L = 0.f;
+  for (int i = 0; i < warps; ++i) L += red[i];
+  for (int i = 0; i + 1 < groups; ++i) {
+    const float4 v = part[i][d4];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
-  const __half2 x = __floats2half2_rn(o[0] * inv, o[1] * inv), y = __floats2half2_rn(o[2] * inv, o[3] * inv);
+  const __half2 x = __floats2half2_rn(o.x * inv, o.y * inv), y = __floats2half2_rn(o.z * inv, o.w * inv);
   *reinterpret_cast<uint2*>(out) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
@@ -789,8 +874,11 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
     e = launch_pdl_cluster(latent_decode_kernel, dim3((unsigned)(2 * l.workers * l.head_tiles)),
                            dim3(kThreads), 2, kSmem, stream, tc, p);
     if (e != cudaSuccess) return e;
+    // Few pairs: each has many segments (the workers' ranges cut them all), and
+    // one group of threads would read them one after another.
+    const bool few = p.num_seqs < l.workers / 4;
     e = launch_pdl(latent_merge_kernel, dim3((unsigned)((long long)p.num_seqs * p.num_heads)),
-                   dim3(128), 0, stream, p);
+                   dim3(few ? 128 * kMergeGroups : 128), 0, stream, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
