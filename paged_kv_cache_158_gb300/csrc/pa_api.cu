@@ -382,7 +382,6 @@ pa_status decode_shared_impl(bool fp8, void* out, const void* query, const void*
     q.num_seqs = num_seqs - q.seq_begin < pa::kMaxSeqsPerLaunch ? num_seqs - q.seq_begin
                                                                 : pa::kMaxSeqsPerLaunch;
     q.counter = p.counter + b;
-    q.inputs_ready = 0;  // the plan of this call is an input
     const size_t smem = pa::decode_smem_bytes(fp8, head_dim, block_size, w.part_tokens, q.num_seqs, true);
     const int per_sm = pa::decode_ctas_per_sm(fp8, head_dim, block_size, smem, false, true);
     long long grid = (long long)per_sm * ds.sms;

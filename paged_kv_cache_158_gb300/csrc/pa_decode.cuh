@@ -527,7 +527,10 @@ __global__ void __launch_bounds__(DecodeTraits<D, B, F8>::THREADS, F8 ? 5 : 1)
   // Item blockIdx.x is this CTA's first; later items come from the counter,
   // numbered from gridDim.x on.
   int cur = blockIdx.x;
-  if (cur >= total) return;
+  if (cur >= total) {
+    if constexpr (SHARED) pdl_wait();  // see the end
+    return;
+  }
 
   // First item's block-table slice (synchronous).
   ItemInfo it = locate_item<B, SHARED>(cur, cum, ctx_s, start_s, nseq, H, P);
@@ -583,7 +586,9 @@ __global__ void __launch_bounds__(DecodeTraits<D, B, F8>::THREADS, F8 ? 5 : 1)
   // Stage of the next issue and of the next consumption (with its phase).
   int st_i = (int)iss % T::NST, st_c = 0;
   uint32_t ph_c = 0;
-  pdl_wait();
+  // SHARED: beside the prefix pass (inputs_ready), which writes nothing that
+  // this one reads or writes; the counter was zeroed by the kernel before it.
+  if constexpr (!SHARED) pdl_wait();
   pdl_launch_dependents();
   // Fetches from the work counter.  Every CTA with a first item fetches once
   // before its loop and once per item it runs, so a launch makes exactly
@@ -824,6 +829,9 @@ __global__ void __launch_bounds__(DecodeTraits<D, B, F8>::THREADS, F8 ? 5 : 1)
     buf ^= 1;
     ++iter;
   }
+  // The merge behind this kernel waits for its end alone, so that has to mean
+  // the prefix pass's end as well.
+  if constexpr (SHARED) pdl_wait();
 }
 
 // Merge the partitions of each (sequence, head): one warp per pair.  The

@@ -10,10 +10,9 @@
 // blocks.  For the two parts' maxima m_a, sums l_a and unnormalised outputs o_a,
 //   out = sum_a 2^(m_a - M) o_a / sum_a 2^(m_a - M) l_a,   M = max m_a.
 //
-// Bound: HBM, the distinct K/V bytes.  A 128-token tile of K and V is 64 KB
-// (D = 128, fp16; 1.5 us of one SM's share of the bandwidth) and feeds two
-// products of up to 128 query rows (0.7 us) and their softmax (0.6 us), which
-// run beside the copies.
+// Bound: HBM, the distinct K/V bytes.  A 64-token tile of K and V is 32 KB
+// (D = 128, fp16; 0.75 us of one SM's share of the bandwidth) and feeds two
+// products of up to 128 query rows (0.3 us) and their softmax (0.6 us).
 //
 // Design (GB300):
 //  * Plan (one CTA): for each group the members whose context covers the
@@ -28,12 +27,17 @@
 //    worker), distinct because along the walk either the unit or w grows.
 //  * Warps: four softmax warps (one query row a thread), TMA, MMA, and for
 //    E4M3 caches four that widen the codes to fp16 in shared memory (exact).
-//    The K/V rings are as deep as the shared memory allows, S is
-//    double-buffered in tensor memory, P (fp16, rounded once) lies over the
-//    first half of its S, and the products of S(t + 1) and P.V(t) are issued
-//    in the order in which they become ready.
+//    The queries are the A operand from tensor memory, S is double-buffered
+//    there, P (fp16, rounded once) lies over the first half of its S, and the
+//    products of S(t + 1) and P.V(t) are issued in the order in which they
+//    become ready.
 //  * Suffix: the decode's partition kernel from each sequence's first own
-//    position on.  Merge: a warp per (sequence, head).
+//    position on.  It runs beside the prefix pass, which waits for its softmax
+//    more than for HBM: it reads nothing of it, so it starts as soon as the
+//    prefix CTAs have, and waits for them only before it ends.  The prefix CTA
+//    is kept small for that (tiles of 64 tokens: 128 KB of shared memory, one
+//    softmax warpgroup), so that decode CTAs fit on its SM.
+//  * Merge: a warp per (sequence, head).
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -49,7 +53,7 @@ namespace pa {
 namespace {
 
 constexpr int kRows = 128;    // query rows of a unit (MMA M)
-constexpr int kTile = 128;    // tokens of a tile
+constexpr int kTile = 64;     // tokens of a tile
 constexpr int kPlanThreads = 1024;
 // Members below which a prefix is not worth a pass of its own.
 constexpr int kMinMembers = 2;
@@ -65,6 +69,7 @@ struct GroupPlan {
 };
 
 struct SharedParams {
+  const void* query;
   const int32_t* group_start;
   const int32_t* prefix_blocks;
   const int32_t* block_tables;
@@ -213,29 +218,31 @@ struct Walk {
 template <int D, bool F8>
 struct Traits {
   static constexpr int NA = D / 64;             // swizzle atoms per row
-  static constexpr int ATOM = 128 * 128;        // 128 rows x 64 fp16
-  static constexpr int TB = kTile * D * 2;      // one fp16 tile of K or V (and the queries)
-  static constexpr int NST = F8 ? 2 : D == 128 ? 3 : 4;
+  static constexpr int ATOM = kTile * 128;      // kTile rows x 64 fp16
+  static constexpr int TB = kTile * D * 2;      // one fp16 tile of K or V
+  static constexpr int NST = F8 ? 2 : 4;
   static constexpr int CB = kTile * D;          // one tile of codes
-  static constexpr int NCS = F8 ? 2 : 0;        // stages of codes (K and V each)
-  static constexpr int OFF_K = TB;
-  static constexpr int OFF_V = OFF_K + NST * TB;
+  static constexpr int NCS = F8 ? 4 : 0;        // stages of codes (K and V each)
+  static constexpr int OFF_V = NST * TB;
   static constexpr int OFF_C = OFF_V + NST * TB;
   static constexpr int OFF_BAR = OFF_C + NCS * 2 * CB;
   static constexpr int USED = OFF_BAR + 512 + 1024;
-  // At least 120 KB, so that one CTA holds an SM (and its 512 TMEM columns).
-  static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
-  static_assert(SMEM <= 232448, "beyond the opt-in shared memory of one CTA");
+  // At least 115 KB, so that two do not share an SM.
+  static constexpr int SMEM = USED > 115 * 1024 ? USED : 115 * 1024;
   static constexpr int THREADS = F8 ? 320 : 192;
-  static constexpr uint32_t COL_O = 256;        // S: 128 columns each; O: D columns
+  static constexpr uint32_t COL_Q = 2 * kTile;  // S: kTile columns each
+  static constexpr uint32_t COL_O = COL_Q + 64; // Q: D / 2 columns; O: D columns
+  static_assert(COL_O + D <= 512, "tensor memory");
 };
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;  // base-2 logits above the reference that move it
 
-// Barriers.
+// Barriers.  S, P and O have one for each parity of the tile: their phases are
+// not all waited for, and S(g) only says that P.V(g - 2) is done, so a single
+// barrier's parity could be taken for the phase before.
 enum {
-  kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = 6, kVFull = 10, kVEmpty = 14, kSFull = 18, kPFull = 20,
-  kOFull = 22, kDone = 23, kCFull = 24 /* K 24, 25; V 26, 27 */, kCEmpty = 28, kNumBars = 32
+  kQFull = 0, kKFull = 1, kKEmpty = 5, kVFull = 9, kVEmpty = 13, kSFull = 17, kPFull = 19, kOFull = 21, kDone = 23,
+  kCFull = 24 /* K 4, V 4 */, kCEmpty = 32 /* K 4, V 4 */, kNumBars = 40
 };
 
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
@@ -268,7 +275,7 @@ __device__ __forceinline__ bool second_first(uint32_t a, uint32_t a_parity, uint
 // thread i of 128 takes 16-code column i % (D/16) of rows i / (D/16) + k * STEP.
 template <int D>
 __device__ __forceinline__ void widen(const unsigned char* src, unsigned char* dst, int i) {
-  constexpr int CPR = D / 16, STEP = 128 / CPR, ATOM = 128 * 128;
+  constexpr int CPR = D / 16, STEP = 128 / CPR, ATOM = kTile * 128;
   static_assert(STEP % 8 == 0, "a thread's rows share one swizzle phase");
   const int j = i % CPR, r0 = i / CPR, c0 = 2 * (j % 4);
   const unsigned char* sp = src + r0 * D + 16 * j;
@@ -284,10 +291,10 @@ __device__ __forceinline__ void widen(const unsigned char* src, unsigned char* d
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
-    shared_prefix_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                         const __grid_constant__ CUtensorMap tv, const SharedParams a) {
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                         const SharedParams a) {
   using T = Traits<D, F8>;
-  constexpr int NST = T::NST;
+  constexpr int NST = T::NST, NCS = F8 ? T::NCS : 1;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -301,11 +308,13 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
   if (tid == 160) {
     for (int i = 0; i < kNumBars; ++i) {
       const bool by_wideners = F8 && ((i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) || i >= kCEmpty);
-      mbar_init(bar(i), i == kPFull || i == kPFull + 1 ? 128 : i == kDone ? T::THREADS : by_wideners ? 4 : 1);
+      mbar_init(bar(i), i == kQFull || i == kPFull || i == kPFull + 1 ? 128
+                        : i == kDone                                  ? T::THREADS
+                        : by_wideners                                 ? 4
+                                                                      : 1);
     }
     *fail = 0;
     fence_mbar_init();
-    prefetch_tensormap(&tq);
     prefetch_tensormap(&tk);
     prefetch_tensormap(&tv);
   }
@@ -338,22 +347,12 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
   }
 
   if (warp == 4) {
-    // ---------------- TMA: a segment's queries, then its K and V tiles
+    // ---------------- TMA: the K and V tiles
     const int bpt = kTile / a.block_size;
-    int g = 0, seg = 0, ki = 0, vi = 0;
+    int g = 0, ki = 0, vi = 0;
     bool ok = true;
     auto uni = [&](bool v) { return __all_sync(kFullMask, v); };
     while (ok && w.next(a)) {
-      if (seg > 0) ok = uni(mbar_wait_bounded(bar(kQEmpty), (seg - 1) & 1));
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar(kQFull), T::TB);
-#pragma unroll
-        for (int at = 0; at < T::NA; ++at)
-          tma_load_3d(s_base + at * T::ATOM, &tq, at * 64, w.h, w.s0, bar(kQFull));
-      }
-      __syncwarp();
-      ++seg;
       const int32_t* bt = a.block_tables + (size_t)w.leader * a.max_blocks;
       auto tile_row = [&](int t) {  // cache row of this lane's block, one tile ahead
         const int lb = t * bpt + lane;
@@ -373,14 +372,14 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
         for (int kv = 0; kv < 2; ++kv) {
           uint32_t dst, full;
           if constexpr (F8) {
-            const int st = g & 1;
-            if (g >= 2) ok = uni(mbar_wait_bounded(bar(kCEmpty + 2 * kv + st), ((g >> 1) - 1) & 1));
-            dst = s_base + T::OFF_C + (2 * kv + st) * T::CB;
-            full = bar(kCFull + 2 * kv + st);
+            const int st = g % NCS;
+            if (g >= NCS) ok = uni(mbar_wait_bounded(bar(kCEmpty + 4 * kv + st), (g / NCS - 1) & 1));
+            dst = s_base + T::OFF_C + (NCS * kv + st) * T::CB;
+            full = bar(kCFull + 4 * kv + st);
           } else {
             const int st = g % NST;
             if (g >= NST) ok = uni(mbar_wait_bounded(bar((kv ? kVEmpty : kKEmpty) + st), (g / NST - 1) & 1));
-            dst = s_base + (kv ? T::OFF_V : T::OFF_K) + st * T::TB;
+            dst = s_base + (kv ? T::OFF_V : 0) + st * T::TB;
             full = bar((kv ? kVFull : kKFull) + st);
           }
           if (!ok) break;
@@ -404,19 +403,17 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
     if (!ok && lane == 0) {
       *fail = 1;
       // The copies in flight land (bounded) before the shared memory goes.
-      if (seg > 0) mbar_wait_bounded(bar(kQFull), (seg - 1) & 1);
-      constexpr int N = F8 ? 2 : NST;
+      constexpr int N = F8 ? NCS : NST;
       for (int u = max(0, ki - N); u < ki; ++u)
         mbar_wait_bounded(bar((F8 ? kCFull : kKFull) + u % N), (u / N) & 1);
       for (int u = max(0, vi - N); u < vi; ++u)
-        mbar_wait_bounded(bar((F8 ? kCFull + 2 : kVFull) + u % N), (u / N) & 1);
+        mbar_wait_bounded(bar((F8 ? kCFull + 4 : kVFull) + u % N), (u / N) & 1);
     }
   } else if (warp == 5) {
     // ---------------- MMA
     constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
     constexpr uint32_t kIdPV = umma_idesc_f16(kRows, D, false, true);
-    const uint64_t q_desc = umma_desc_sw128(s_base, 16, 1024);
-    const uint64_t k_desc = umma_desc_sw128(s_base + T::OFF_K, 16, 1024);
+    const uint64_t k_desc = umma_desc_sw128(s_base, 16, 1024);
     const uint64_t v_desc = umma_desc_sw128(s_base + T::OFF_V, T::ATOM, 1024);
     constexpr uint64_t kStep = (uint64_t)T::TB >> 4;
     auto uni = [&](bool v) { return __all_sync(kFullMask, v); };
@@ -431,10 +428,10 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          umma_f16_tmem_a(tmem + T::COL_O, tmem + 128 * (g & 1) + 8 * k,
+          umma_f16_tmem_a(tmem + T::COL_O, tmem + kTile * (g & 1) + 8 * k,
                           vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV, !first || k > 0);
         umma_commit(bar(kVEmpty + g % NST));
-        umma_commit(bar(kOFull));
+        umma_commit(bar(kOFull + (g & 1)));
       }
       __syncwarp();
       ++pv;
@@ -443,11 +440,14 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
     int g = 0, seg = 0;
     bool ok = true, prev_first = false;
     while (ok && w.next(a)) {
-      ok = uni(mbar_wait_bounded(bar(kQFull), seg & 1));
+      // The next queries come after the last segment's output, so its last P.V
+      // goes first.
+      if (pv < g) ok = pv_mma(g - 1, prev_first);
+      ok = ok && uni(mbar_wait_bounded(bar(kQFull), seg & 1));
       for (int t = w.t_begin; ok && t < w.t_end; ++t, ++g) {
         const int st = g % NST;
         // Of S(t) and P.V of the tile before, the one that can start first.
-        if (g > 0 && second_first(bar(kKFull + st), (g / NST) & 1, bar(kPFull + ((g - 1) & 1)), ((g - 1) >> 1) & 1))
+        if (pv < g && second_first(bar(kKFull + st), (g / NST) & 1, bar(kPFull + ((g - 1) & 1)), ((g - 1) >> 1) & 1))
           ok = pv_mma(g - 1, prev_first);
         ok = ok && uni(mbar_wait_bounded(bar(kKFull + st), (g / NST) & 1));
         if (!ok) break;
@@ -457,11 +457,10 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint64_t off = (uint64_t)(((k / 4) * T::ATOM + (k % 4) * 32) >> 4);
-            umma_f16(tmem + 128 * (g & 1), q_desc + off, kd + off, kIdQK, k > 0);
+            umma_f16_tmem_a(tmem + kTile * (g & 1), tmem + T::COL_Q + 8 * k, kd + off, kIdQK, k > 0);
           }
           umma_commit(bar(kSFull + (g & 1)));
           umma_commit(bar(kKEmpty + st));
-          if (t + 1 == w.t_end) umma_commit(bar(kQEmpty));  // the queries' last reader
         }
         __syncwarp();
         ++qk;
@@ -476,7 +475,7 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
       *fail = 1;
       // Every product started ends (bounded) before its memory goes.
       if (qk > 0) mbar_wait_bounded(bar(kSFull + ((qk - 1) & 1)), ((qk - 1) >> 1) & 1);
-      if (pv > 0) mbar_wait_bounded(bar(kOFull), (pv - 1) & 1);
+      if (pv > 0) mbar_wait_bounded(bar(kOFull + ((pv - 1) & 1)), ((pv - 1) >> 1) & 1);
     }
   } else if (warp < 4) {
     // ---------------- softmax: one query row a thread
@@ -486,9 +485,31 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
     bool ok = true;
     while (ok && w.next(a)) {
       const bool live = warp * 32 < w.rows;  // this warp has members
+      // The queries to tensor memory (the last segment's Q K^T products are
+      // done: their S has been read).  Rows past the members are zero.
+      if (live) {
+        const uint4* q = reinterpret_cast<const uint4*>(
+            static_cast<const __half*>(a.query) + ((size_t)(w.s0 + (row < w.rows ? row : 0)) * a.num_heads + w.h) * D);
+#pragma unroll
+        for (int cb = 0; cb < T::NA; ++cb) {
+          uint32_t r[32];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 v = row < w.rows ? q[cb * 8 + c] : make_uint4(0, 0, 0, 0);
+            r[4 * c] = v.x;
+            r[4 * c + 1] = v.y;
+            r[4 * c + 2] = v.z;
+            r[4 * c + 3] = v.w;
+          }
+          tmem_st32(tmem + t_lane + T::COL_Q + 32 * cb, r);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      mbar_arrive(bar(kQFull));
       float m = -INFINITY, l = 0.f;
       for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
-        const uint32_t t_s = tmem + t_lane + 128 * (g & 1);
+        const uint32_t t_s = tmem + t_lane + kTile * (g & 1);
         ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kSFull + (g & 1)), (g >> 1) & 1) && !*fail);
         if (!ok) break;
         if (live) {
@@ -531,7 +552,7 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
           l = l * alpha + ((sq[0] + sq[1]) + (sq[2] + sq[3]));
           if (t > w.t_begin && __any_sync(kFullMask, alpha != 1.f)) {
             // O holds the tiles up to t - 1 once P.V of t - 1 is done.
-            ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kOFull), (g - 1) & 1) && !*fail);
+            ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kOFull + ((g - 1) & 1)), ((g - 1) >> 1) & 1) && !*fail);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -544,10 +565,7 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
               tmem_st32(tmem + t_lane + T::COL_O + cb * 32, r);
             }
           }
-          // P over the first 64 columns of its S.
-#pragma unroll
-          for (int cb = 0; cb < 2; ++cb)
-            tmem_st32(t_s + cb * 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[cb * 32]));
+          tmem_st32(t_s, pk);  // P over the first half of its S
           tmem_wait_st();
           tc_fence_before();
         }
@@ -555,7 +573,7 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
       }
       if (!ok) break;
       // The segment's partial rows.
-      ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kOFull), (g - 1) & 1) && !*fail);
+      ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kOFull + ((g - 1) & 1)), ((g - 1) >> 1) & 1) && !*fail);
       if (!ok) break;
       if (live) {
         tc_fence_after();
@@ -586,18 +604,18 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
     bool ok = true;
     while (ok && w.next(a)) {
       for (int t = w.t_begin; ok && t < w.t_end; ++t, ++g) {
-        const int cs = g & 1, st = g % NST;
+        const int cs = g % NCS, st = g % NST;
 #pragma unroll
         for (int kv = 0; kv < 2 && ok; ++kv) {
-          ok = mbar_wait_bounded(bar(kCFull + 2 * kv + cs), (g >> 1) & 1);
+          ok = mbar_wait_bounded(bar(kCFull + 4 * kv + cs), (g / NCS) & 1);
           if (g >= NST) ok = ok && mbar_wait_bounded(bar((kv ? kVEmpty : kKEmpty) + st), (g / NST - 1) & 1);
           ok = __all_sync(kFullMask, ok && !*fail);
           if (!ok) break;
-          widen<D>(sm + T::OFF_C + (2 * kv + cs) * T::CB, sm + (kv ? T::OFF_V : T::OFF_K) + st * T::TB, i);
+          widen<D>(sm + T::OFF_C + (NCS * kv + cs) * T::CB, sm + (kv ? T::OFF_V : 0) + st * T::TB, i);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(bar(kCEmpty + 2 * kv + cs));
+            mbar_arrive(bar(kCEmpty + 4 * kv + cs));
             mbar_arrive(bar((kv ? kVFull : kKFull) + st));
           }
         }
@@ -713,6 +731,7 @@ Layout layout(int S, int G, int H, int D, int sms) {
 SharedParams params(const SharedArgs& g) {
   const Layout l = layout(g.num_seqs, g.num_groups, g.dec.num_heads, g.head_dim, g.sms);
   SharedParams p{};
+  p.query = g.dec.query;
   p.group_start = g.group_start;
   p.prefix_blocks = g.prefix_blocks;
   p.block_tables = g.dec.block_tables;
@@ -763,19 +782,14 @@ cudaError_t launch_prefix_t(const SharedArgs& g, SharedParams p, cudaStream_t st
   const int H = g.dec.num_heads;
   const long long rows = (long long)g.dec.num_blocks * H * g.block_size;
   p.oob_row = (int)rows;
-  CUtensorMap tq, tk, tv;
-  const cuuint64_t qdims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)g.num_seqs};
-  const cuuint64_t qstr[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
-  const cuuint32_t qbox[3] = {64, 1, (cuuint32_t)kRows};
+  CUtensorMap tk, tv;
   const cuuint64_t kdims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
   const cuuint64_t kstr[1] = {(cuuint64_t)D * (F8 ? 1 : 2)};
   const cuuint32_t kbox[2] = {(cuuint32_t)(F8 ? D : 64), (cuuint32_t)g.block_size};
-  if (!encode_tensor_map(&tq, g.dec.query, 3, qdims, qstr, qbox) ||
-      !encode_tensor_map(&tk, g.dec.key_cache, 2, kdims, kstr, kbox, F8) ||
+  if (!encode_tensor_map(&tk, g.dec.key_cache, 2, kdims, kstr, kbox, F8) ||
       !encode_tensor_map(&tv, g.dec.value_cache, 2, kdims, kstr, kbox, F8))
     return cudaErrorInvalidValue;
-  return launch_pdl(shared_prefix_kernel<D, F8>, dim3(p.workers), dim3(T::THREADS), T::SMEM, stream, tq, tk,
-                    tv, p);
+  return launch_pdl(shared_prefix_kernel<D, F8>, dim3(p.workers), dim3(T::THREADS), T::SMEM, stream, tk, tv, p);
 }
 
 }  // namespace
@@ -787,6 +801,9 @@ size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_heads, int h
 cudaError_t launch_shared_prefix(SharedArgs& g, cudaStream_t stream) {
   const SharedParams p = params(g);
   g.dec.seq_start = p.seq_start;
+  // The prefix pass starts after the plan has ended; behind it, the suffix pass
+  // finds the plan complete.
+  g.dec.inputs_ready = p.num_groups > 0 && p.max_prefix_blocks > 0;
   const cudaError_t e = launch_pdl(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
   if (e != cudaSuccess || p.num_groups == 0 || p.max_prefix_blocks == 0) return e;
   if (g.fp8)
