@@ -777,6 +777,10 @@ cudaError_t launch_prefix_t(const SharedArgs& g, SharedParams p, cudaStream_t st
   if (dev > 63 || !(prepared.load(std::memory_order_acquire) >> dev & 1)) {
     e = cudaFuncSetAttribute(shared_prefix_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
     if (e != cudaSuccess) return e;
+    // All of the SM's shared memory, so that suffix CTAs fit beside this one.
+    e = cudaFuncSetAttribute(shared_prefix_kernel<D, F8>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
     if (dev <= 63) prepared.fetch_or(1ull << dev, std::memory_order_release);
   }
   const int H = g.dec.num_heads;
