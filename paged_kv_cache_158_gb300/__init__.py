@@ -133,9 +133,13 @@ def _check(status: int, what: str) -> None:
         raise PAError(status, what)
 
 
+# The current stream's handle without building a torch.cuda.Stream around it (0.1 us against 2.9).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -511,12 +515,13 @@ def pa_slot_mapping(slot_mapping: torch.Tensor, block_tables: torch.Tensor, toke
     _check(st, "pa_slot_mapping")
 
 
-def _same_device(*tensors) -> None:
-    """The library launches on the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+def _ptr_on(dev: int, t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
+    """_ptr of a tensor that has to be on device `dev` (the library launches on the current one);
+    one pass of cheap attribute reads, the message only where one fails."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, name, dtype)
+    raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
 
 
 def pa_decode_shared_workspace_size(num_seqs: int, num_groups: int, num_heads: int, head_dim: int,
@@ -560,23 +565,26 @@ def pa_decode_shared_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torc
 def _decode_shared(out, query, key_cache, value_cache, block_tables, context_lens, group_start,
                    prefix_blocks, scale, fp8, max_context_len, max_prefix_len, workspace, stream) -> None:
     S, H, D, B, NB = _decode_shapes(out, query, key_cache, value_cache, block_tables, context_lens)
-    G = prefix_blocks.shape[0]
-    if group_start.shape != (G + 1,) or prefix_blocks.dim() != 1:
+    G, = prefix_blocks.shape
+    if group_start.shape != (G + 1,):
         raise ValueError("group_start must be [num_groups + 1] and prefix_blocks [num_groups]")
-    _same_device(out, query, key_cache, value_cache, block_tables, context_lens, group_start,
-                 prefix_blocks, workspace)
-    name = "pa_decode_shared" if fp8 is None else "pa_decode_shared_fp8"
-    st = getattr(_lib, name)(_ptr(out, "out", torch.float16), _ptr(query, "query", torch.float16),
-                             _cache_ptr(key_cache, "key_cache", fp8 is not None),
-                             _cache_ptr(value_cache, "value_cache", fp8 is not None),
-                             _ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1],
-                             _ptr(context_lens, "context_lens", torch.int32),
-                             _ptr(group_start, "group_start", torch.int32),
-                             _ptr(prefix_blocks, "prefix_blocks", torch.int32), G, S, H, D, B, NB,
-                             float(scale), *(fp8 or ()), int(max_context_len), int(max_prefix_len),
-                             _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
-                             _stream(stream))
-    _check(st, name)
+    dev, i32, f16 = torch.cuda.current_device(), torch.int32, torch.float16
+    fn, cache, scales = _lib.pa_decode_shared, f16, ()
+    if fp8 is not None:
+        fn, cache, scales = _lib.pa_decode_shared_fp8, torch.uint8, fp8
+        if key_cache.dtype == torch.float8_e4m3fn:
+            key_cache = key_cache.view(torch.uint8)
+        if value_cache.dtype == torch.float8_e4m3fn:
+            value_cache = value_cache.view(torch.uint8)
+    st = fn(_ptr_on(dev, out, "out", f16), _ptr_on(dev, query, "query", f16),
+            _ptr_on(dev, key_cache, "key_cache", cache), _ptr_on(dev, value_cache, "value_cache", cache),
+            _ptr_on(dev, block_tables, "block_tables", i32), block_tables.shape[1],
+            _ptr_on(dev, context_lens, "context_lens", i32),
+            _ptr_on(dev, group_start, "group_start", i32),
+            _ptr_on(dev, prefix_blocks, "prefix_blocks", i32), G, S, H, D, B, NB, float(scale), *scales,
+            int(max_context_len), int(max_prefix_len), _ptr_on(dev, workspace, "workspace", torch.uint8),
+            workspace.numel(), _raw_stream(dev) if stream is None else _stream(stream))
+    _check(st, "pa_decode_shared" if fp8 is None else "pa_decode_shared_fp8")
 
 
 def pa_build_tables_workspace_size(num_seqs: int) -> int:
@@ -599,45 +607,47 @@ def pa_build_tables(block_tables: torch.Tensor, context_lens: torch.Tensor, quer
     lengths [S], taking blocks from the end of free_list[:num_free]; sequences of a group share
     its leading prefix_blocks (see pa_build_tables in include/pa.h).  context_lens may be
     cached_lens and num_free_out may be num_free."""
-    S = cached_lens.shape[0]
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or \
-            new_lens.shape != (S,) or query_start.shape != (S + 1,) or slot_mapping.dim() != 1 or \
-            free_list.dim() != 1 or num_free.numel() != 1 or num_free_out.numel() != 1:
+    S, = cached_lens.shape
+    S2, W = block_tables.shape
+    T, = slot_mapping.shape
+    F, = free_list.shape
+    if S2 != S or context_lens.shape != (S,) or new_lens.shape != (S,) or \
+            query_start.shape != (S + 1,) or num_free.numel() != 1 or num_free_out.numel() != 1:
         raise ValueError("shape mismatch")
     if (group_start is None) != (prefix_blocks is None):
         raise ValueError("group_start and prefix_blocks go together")
-    G = 0
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    G, gs, pb = 0, None, None
     if prefix_blocks is not None:
-        G = prefix_blocks.shape[0]
+        G, = prefix_blocks.shape
         if group_start.shape != (G + 1,):
             raise ValueError("group_start must be [num_groups + 1]")
-    _same_device(block_tables, context_lens, query_start, slot_mapping, num_free_out, free_list,
-                 num_free, cached_lens, new_lens, workspace, group_start, prefix_blocks)
-    st = _lib.pa_build_tables(_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1],
-                              _ptr(context_lens, "context_lens", torch.int32),
-                              _ptr(query_start, "query_start", torch.int32),
-                              _ptr(slot_mapping, "slot_mapping", torch.int64), slot_mapping.shape[0],
-                              _ptr(num_free_out, "num_free_out", torch.int32),
-                              _ptr(free_list, "free_list", torch.int32), free_list.shape[0],
-                              _ptr(num_free, "num_free", torch.int32),
-                              _ptr(cached_lens, "cached_lens", torch.int32),
-                              _ptr(new_lens, "new_lens", torch.int32),
-                              _ptr(group_start, "group_start", torch.int32) if G else None,
-                              _ptr(prefix_blocks, "prefix_blocks", torch.int32) if G else None, G, S,
+        if G:
+            gs = _ptr_on(dev, group_start, "group_start", i32)
+            pb = _ptr_on(dev, prefix_blocks, "prefix_blocks", i32)
+    st = _lib.pa_build_tables(_ptr_on(dev, block_tables, "block_tables", i32), W,
+                              _ptr_on(dev, context_lens, "context_lens", i32),
+                              _ptr_on(dev, query_start, "query_start", i32),
+                              _ptr_on(dev, slot_mapping, "slot_mapping", torch.int64), T,
+                              _ptr_on(dev, num_free_out, "num_free_out", i32),
+                              _ptr_on(dev, free_list, "free_list", i32), F,
+                              _ptr_on(dev, num_free, "num_free", i32),
+                              _ptr_on(dev, cached_lens, "cached_lens", i32),
+                              _ptr_on(dev, new_lens, "new_lens", i32), gs, pb, G, S,
                               int(block_size), int(num_blocks),
-                              _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
-                              _stream(stream))
+                              _ptr_on(dev, workspace, "workspace", torch.uint8), workspace.numel(),
+                              _raw_stream(dev) if stream is None else _stream(stream))
     _check(st, "pa_build_tables")
 
 
-def _rows_ptr(t: torch.Tensor, name: str) -> int:
+def _rows_ptr(dev: int, t: torch.Tensor, name: str) -> int:
     """fp16 rows whose values are adjacent; the rows may be apart (a slice of a wider array)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.float16:
+    if t.dtype is not torch.float16:
         raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name} must be [T, n] with adjacent values")
     return t.data_ptr()
@@ -648,16 +658,16 @@ def pa_latent_write(latent: torch.Tensor, rope: torch.Tensor, cache: torch.Tenso
     """Scatter latent rows (latent [T,512], rope [T,64]; either may be a slice of a wider array)
     into their slots of the latent cache [NB,B,576] (see pa_latent_write in include/pa.h)."""
     T, L = latent.shape
-    R = rope.shape[1]
+    T2, R = rope.shape
     NB, B, W = cache.shape
-    if rope.shape[0] != T or W != L + R or slot_mapping.shape != (T,):
+    if T2 != T or W != L + R or slot_mapping.shape != (T,):
         raise ValueError("shape mismatch")
-    _same_device(latent, rope, cache, slot_mapping)
-    st = _lib.pa_latent_write(_rows_ptr(latent, "latent"), latent.stride(0) if T > 1 else L,
-                              _rows_ptr(rope, "rope"), rope.stride(0) if T > 1 else R,
-                              _ptr(cache, "cache", torch.float16),
-                              _ptr(slot_mapping, "slot_mapping", torch.int64), T, L, R, B, NB,
-                              _stream(stream))
+    dev = torch.cuda.current_device()
+    st = _lib.pa_latent_write(_rows_ptr(dev, latent, "latent"), latent.stride(0) if T > 1 else L,
+                              _rows_ptr(dev, rope, "rope"), rope.stride(0) if T > 1 else R,
+                              _ptr_on(dev, cache, "cache", torch.float16),
+                              _ptr_on(dev, slot_mapping, "slot_mapping", torch.int64), T, L, R, B,
+                              NB, _raw_stream(dev) if stream is None else _stream(stream))
     _check(st, "pa_latent_write")
 
 
@@ -680,19 +690,19 @@ def pa_latent_decode(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor
     [NB,B,576] (see pa_latent_decode in include/pa.h)."""
     S, H, W = query.shape
     NB, B, W2 = cache.shape
-    L = out.shape[2]
-    if W2 != W or tuple(out.shape) != (S, H, L) or block_tables.dim() != 2 or \
-            block_tables.shape[0] != S or context_lens.shape != (S,):
+    S2, H2, L = out.shape
+    S3, MB = block_tables.shape
+    if W2 != W or S2 != S or H2 != H or S3 != S or context_lens.shape != (S,):
         raise ValueError("shape mismatch")
-    _same_device(out, query, cache, block_tables, context_lens, workspace)
-    st = _lib.pa_latent_decode(_ptr(out, "out", torch.float16), _ptr(query, "query", torch.float16),
-                               _ptr(cache, "cache", torch.float16),
-                               _ptr(block_tables, "block_tables", torch.int32),
-                               block_tables.shape[1],
-                               _ptr(context_lens, "context_lens", torch.int32), S, H, L, W - L, B, NB,
-                               float(scale), int(max_context_len),
-                               _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
-                               _stream(stream))
+    dev = torch.cuda.current_device()
+    st = _lib.pa_latent_decode(_ptr_on(dev, out, "out", torch.float16),
+                               _ptr_on(dev, query, "query", torch.float16),
+                               _ptr_on(dev, cache, "cache", torch.float16),
+                               _ptr_on(dev, block_tables, "block_tables", torch.int32), MB,
+                               _ptr_on(dev, context_lens, "context_lens", torch.int32), S, H, L,
+                               W - L, B, NB, float(scale), int(max_context_len),
+                               _ptr_on(dev, workspace, "workspace", torch.uint8), workspace.numel(),
+                               _raw_stream(dev) if stream is None else _stream(stream))
     _check(st, "pa_latent_decode")
 
 
