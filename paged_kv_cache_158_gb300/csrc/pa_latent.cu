@@ -709,10 +709,88 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the segments of each (sequence, head): with M = max m_i,
 //   out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
-// One CTA a pair; 128 threads, four values each, take the segments in turn with
-// the other groups of 128 (few pairs with many segments need several; the
-// order of the sums goes by the batch's shape alone).  A sequence of no tokens
-// gets zeros, one that a single worker covered is already written.
+// A sequence of no tokens gets zeros, one that a single worker covered is
+// already written.  Two forms, by the batch's shape alone (the order of the
+// sums is part of the result): many sequences have few segments each, and a
+// warp takes a pair; of few sequences each has many segments, and a CTA takes a
+// pair, its groups of 128 threads the segments in turn.  (64 sequences of
+// 4096-8192 tokens, 128 heads: 25 us by CTAs; two of 60-100 thousand tokens, 64
+// heads: 19 us with one group, 3 us with four.)
+
+// Where the partials of pair (s, h) are; false: nothing to join.
+__device__ __forceinline__ bool merge_segments(const LatentParams& a, int s, int h, bool* empty, size_t* base, int* n) {
+  const int c0 = a.cum[s], c1 = a.cum[s + 1], total = a.cum[a.num_seqs];
+  *empty = c0 == c1;
+  if (*empty) return false;
+  const int W = active_workers(a, total);
+  const int w0 = worker_of(c0, W, total), w1 = worker_of(c1 - 1, W, total);
+  *n = w1 - w0 + 1;
+  *base = (size_t)(s + w0) * a.num_heads + h;
+  return *n > 1;
+}
+
+__device__ __forceinline__ uint2 half4(const float4& v, float inv) {
+  const __half2 x = __floats2half2_rn(v.x * inv, v.y * inv), y = __floats2half2_rn(v.z * inv, v.w * inv);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+
+__device__ __forceinline__ void fma4(float4& o, float x, const float4& v) {
+  o.x = fmaf(x, v.x, o.x);
+  o.y = fmaf(x, v.y, o.y);
+  o.z = fmaf(x, v.z, o.z);
+  o.w = fmaf(x, v.w, o.w);
+}
+
+// A warp a pair: lane l has values 4 l + 128 j, j < 4.
+__global__ void __launch_bounds__(128) latent_merge_warp_kernel(const LatentParams a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long pair = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (pair >= (long long)a.num_seqs * a.num_heads) return;
+  const int s = (int)(pair / a.num_heads), h = (int)(pair - (long long)s * a.num_heads);
+  __half* out = static_cast<__half*>(a.out) + ((size_t)(a.seq_begin + s) * a.num_heads + h) * kLatentDim + 4 * lane;
+  bool empty;
+  size_t base;
+  int n;
+  if (!merge_segments(a, s, h, &empty, &base, &n)) {
+    if (empty)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint2*>(out + 128 * j) = make_uint2(0, 0);
+    return;
+  }
+  const float2* ml = a.ws_ml + base;
+  const float* src = a.ws_o + base * kLatentDim + 4 * lane;
+  const size_t step = (size_t)a.num_heads * kLatentDim;
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[(size_t)i * a.num_heads].x);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+  float L = 0.f;
+  float4 o[4] = {};
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float wt = 0.f;
+    if (i0 + lane < n) {
+      const float2 x = ml[(size_t)(i0 + lane) * a.num_heads];
+      wt = x.x == -INFINITY ? 0.f : exp2_approx(x.x - M);
+      L = fmaf(wt, x.y, L);
+    }
+    const int cnt = min(32, n - i0);
+#pragma unroll 2
+    for (int i = 0; i < cnt; ++i) {
+      const float x = __shfl_sync(kFullMask, wt, i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        fma4(o[j], x, *reinterpret_cast<const float4*>(src + (i0 + i) * step + 128 * j));
+    }
+  }
+#pragma unroll
+  for (int k = 16; k >= 1; k >>= 1) L += __shfl_xor_sync(kFullMask, L, k);
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint2*>(out + 128 * j) = half4(o[j], inv);
+}
+
 constexpr int kMergeGroups = 4;
 constexpr int kMergeChunk = 128;  // segments whose weights are held at a time
 
@@ -722,21 +800,19 @@ __global__ void __launch_bounds__(128 * kMergeGroups) latent_merge_kernel(const 
   __shared__ float4 part[kMergeGroups - 1][128];
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, group = tid >> 7, groups = (int)blockDim.x >> 7, d4 = tid & 127;
-  const int warp = tid >> 5, lane = tid & 31, warps = (int)blockDim.x >> 5;
+  constexpr int groups = kMergeGroups, warps = 4 * kMergeGroups;
+  const int tid = threadIdx.x, group = tid >> 7, d4 = tid & 127;
+  const int warp = tid >> 5, lane = tid & 31;
   const int s = (int)blockIdx.x / a.num_heads, h = (int)blockIdx.x - s * a.num_heads;
-  const int c0 = a.cum[s], c1 = a.cum[s + 1], total = a.cum[a.num_seqs];
   __half* out = static_cast<__half*>(a.out) +
                 ((size_t)(a.seq_begin + s) * a.num_heads + h) * kLatentDim + 4 * d4;
-  if (c0 == c1) {
-    if (group == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
+  bool empty;
+  size_t base;
+  int n;
+  if (!merge_segments(a, s, h, &empty, &base, &n)) {
+    if (empty && group == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
     return;
   }
-  const int W = active_workers(a, total);
-  const int w0 = worker_of(c0, W, total), w1 = worker_of(c1 - 1, W, total);
-  if (w0 == w1) return;
-  const int n = w1 - w0 + 1;
-  const size_t base = (size_t)(s + w0) * a.num_heads + h;
   auto block_max = [&](float v) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
@@ -747,7 +823,7 @@ __global__ void __launch_bounds__(128 * kMergeGroups) latent_merge_kernel(const 
     return v;
   };
   float M = -INFINITY;
-  for (int i = tid; i < n; i += (int)blockDim.x) M = fmaxf(M, a.ws_ml[base + (size_t)i * a.num_heads].x);
+  for (int i = tid; i < n; i += 128 * kMergeGroups) M = fmaxf(M, a.ws_ml[base + (size_t)i * a.num_heads].x);
   M = block_max(M);
   float L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -764,12 +840,7 @@ __global__ void __launch_bounds__(128 * kMergeGroups) latent_merge_kernel(const 
     const size_t step = (size_t)a.num_heads * kLatentDim;
 #pragma unroll 8
     for (int i = group; i < cnt; i += groups) {
-      const float4 v = *reinterpret_cast<const float4*>(src + i * step);
-      const float x = wt_s[i];
-      o.x = fmaf(x, v.x, o.x);
-      o.y = fmaf(x, v.y, o.y);
-      o.z = fmaf(x, v.z, o.z);
-      o.w = fmaf(x, v.w, o.w);
+      fma4(o, wt_s[i], *reinterpret_cast<const float4*>(src + i * step));
     }
     __syncthreads();
   }
@@ -781,17 +852,8 @@ __global__ void __launch_bounds__(128 * kMergeGroups) latent_merge_kernel(const 
   if (group > 0) return;
   L = 0.f;
   for (int i = 0; i < warps; ++i) L += red[i];
-  for (int i = 0; i + 1 < groups; ++i) {
-    const float4 v = part[i][d4];
-    o.x += v.x;
-    o.y += v.y;
-    o.z += v.z;
-    o.w += v.w;
-  }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  const __half2 x = __floats2half2_rn(o.x * inv, o.y * inv), y = __floats2half2_rn(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2*>(out) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  for (int i = 0; i + 1 < groups; ++i) fma4(o, 1.f, part[i][d4]);
+  *reinterpret_cast<uint2*>(out) = half4(o, L > 0.f ? 1.f / L : 0.f);
 }
 
 struct LatentLayout {
@@ -874,11 +936,10 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
     e = launch_pdl_cluster(latent_decode_kernel, dim3((unsigned)(2 * l.workers * l.head_tiles)),
                            dim3(kThreads), 2, kSmem, stream, tc, p);
     if (e != cudaSuccess) return e;
-    // Few pairs: each has many segments (the workers' ranges cut them all), and
-    // one group of threads would read them one after another.
-    const bool few = p.num_seqs < l.workers / 4;
-    e = launch_pdl(latent_merge_kernel, dim3((unsigned)((long long)p.num_seqs * p.num_heads)),
-                   dim3(few ? 128 * kMergeGroups : 128), 0, stream, p);
+    const long long pairs = (long long)p.num_seqs * p.num_heads;
+    e = p.num_seqs < l.workers / 4
+            ? launch_pdl(latent_merge_kernel, dim3((unsigned)pairs), dim3(128 * kMergeGroups), 0, stream, p)
+            : launch_pdl(latent_merge_warp_kernel, dim3((unsigned)((pairs + 3) / 4)), dim3(128), 0, stream, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
