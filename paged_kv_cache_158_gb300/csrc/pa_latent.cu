@@ -38,10 +38,10 @@
 //  * The queries (fp16, 144 columns) are the A operand of Q K^T from tensor
 //    memory, so a product of 64 tokens reads 2 KB of shared memory, not 6, and
 //    the shared memory holds four stages of rows.
-//  * A stage is 64 rows of the CTA's 256 latent values and the 64 rotary ones
-//    (five 64-value swizzle atoms), copied by TMA one box a block and atom; it
-//    is the K operand of Q K^T and, its first four atoms read the other way
-//    round, the V operand of P V.
+//  * A stage is 64 rows of the CTA's 256 latent values (four 64-value atoms of
+//    128-byte swizzle) and its 32 rotary ones (64-byte swizzle), copied by TMA
+//    one box a block and atom; it is the K operand of Q K^T and, its four atoms
+//    read the other way round, the V operand of P V.
 //  * Two softmax warpgroups (one head row a thread) take alternate tiles, so
 //    one's exchange overlaps the other's exponentials.  The row's reference
 //    goes from tile to tile through shared memory; each group keeps the sum of
@@ -97,9 +97,10 @@ __global__ void __launch_bounds__(256)
 constexpr int kRows = 128;             // head rows of a cluster (MMA M)
 constexpr int kTile = 64;              // tokens of a tile
 constexpr int kHalf = kLatentDim / 2;  // output values of a CTA
-constexpr int kAtoms = 5;              // its 64-value atoms: four latent, the rotary one
+constexpr int kAtoms = 4;              // its 64-value atoms of latent values
 constexpr int kAtomBytes = kTile * 128;
-constexpr int kStageBytes = kAtoms * kAtomBytes;
+constexpr int kRopeBytes = kTile * kRopeDim;  // its half of the rotary values
+constexpr int kStageBytes = kAtoms * kAtomBytes + kRopeBytes;
 constexpr int kStages = 4;
 constexpr int kThreads = 320;          // two softmax warpgroups, TMA, MMA
 constexpr int kWarpTma = 8, kWarpMma = 9;
@@ -107,7 +108,8 @@ constexpr int kSeqsPerLaunch = 1024;
 
 constexpr int kXBytes = kRows * kTile * 4;                 // one half of S from the other CTA
 constexpr int kOffX = kStages * kStageBytes;               // buffer b at kOffX + b * kXBytes
-constexpr int kOffBar = kOffX + 2 * kXBytes;
+constexpr int kOffP = kOffX + 2 * kXBytes;                 // P of odd tiles
+constexpr int kOffBar = kOffP + kRows * kTile * 2;
 constexpr int kOffRef = kOffBar + 256;                     // float [128]: each row's reference
 constexpr int kOffMl = kOffRef + kRows * 4;                // float2 [2][128]: reference and sum of each group
 constexpr int kSmem = kOffMl + 2 * kRows * 8;
@@ -116,16 +118,16 @@ static_assert(kSmem <= 232448, "beyond the opt-in shared memory of one CTA");
 constexpr uint32_t kTmemCols = 512;    // O: [0, 256)
 constexpr uint32_t kColQ = 256;        // queries: 128 columns latent, 16 rotary (and 16 unused)
 constexpr uint32_t kColS = 416;        // 64
-constexpr uint32_t kColP = 480;        // 32
+constexpr uint32_t kColP = 480;        // 32: P of even tiles (odd ones: shared memory, for want of columns)
 
 constexpr float kRescale = 8.f;        // base-2 logits above the reference that move it
 
 // Barriers.  Those of two phases at a time that one warpgroup sees every
 // other one of come in pairs, by the tile's parity.
 enum {
-  kKFull = 0 /* 4 */, kKEmpty = 4 /* 4 */, kQFull = 8, kSFull = 9 /* 2 */, kSFree = 11, kPFull = 12,
-  kOFull = 13 /* 2 */, kXFull = 15 /* 2 */, kXFree = 17 /* 2 */, kRef = 19 /* 2 */, kSegA = 21, kSegB = 22, kDone = 23,
-  kNumBars = 24
+  kKFull = 0 /* 4 */, kKEmpty = 4 /* 4 */, kQFull = 8, kSFull = 9 /* 2 */, kSFree = 11, kPFull = 12 /* 2 */,
+  kOFull = 14 /* 2 */, kXFull = 16 /* 2 */, kXFree = 18 /* 2 */, kRef = 20 /* 2 */, kSegA = 22, kSegB = 23, kDone = 24,
+  kNumBars = 25
 };
 
 struct LatentParams {
@@ -229,7 +231,7 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
 
 // Bounded wait on a barrier that the other CTA completes.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
+  uint64_t t0 = 0;
   while (true) {
     uint32_t ok;
     asm volatile(
@@ -242,7 +244,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity)
         : "r"(bar), "r"(parity)
         : "memory");
     if (ok) return true;
-    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) return false;
   }
 }
 
@@ -253,7 +257,8 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_decode_kernel(const __grid_constant__ CUtensorMap tc, const LatentParams a) {
+    latent_decode_kernel(const __grid_constant__ CUtensorMap tc, const __grid_constant__ CUtensorMap tr,
+                         const LatentParams a) {
   extern __shared__ __align__(1024) unsigned char sm[];  // the swizzle's phase is the address's
   const uint32_t s_base = smem_u32(sm);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
@@ -270,14 +275,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int live_warps = min(4, (a.num_heads - h0 + 31) / 32);  // softmax warps with heads
   if (tid == kWarpMma * 32) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i == kSFree || i == kPFull || i == kRef || i == kRef + 1 ? 128
-                        : i == kQFull || i == kSegA || i == kSegB                 ? 256
-                        : i == kXFree || i == kXFree + 1                          ? live_warps
-                        : i == kDone                                              ? kThreads
-                                                                                  : 1);
+      mbar_init(bar(i), i == kSFree || i == kPFull || i == kPFull + 1 || i == kRef || i == kRef + 1 ? 128
+                        : i == kQFull || i == kSegA || i == kSegB                                    ? 256
+                        : i == kXFree || i == kXFree + 1                                             ? live_warps
+                        : i == kDone                                                                 ? kThreads
+                                                                                                     : 1);
     *fail = 0;
     fence_mbar_init();
     prefetch_tensormap(&tc);
+    prefetch_tensormap(&tr);
   }
   if (warp == kWarpTma) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();  // the other CTA's barriers exist
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(kFullMask, *tmem_slot, 0);
   Walk w;
   w.s = start[0];
   w.t = start[1];
@@ -362,11 +368,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + st), kStageBytes);
         __syncwarp();
-        const uint32_t dst = s_base + st * kStageBytes + b * a.block_size * 128;
-        for (int i = lane; i < kAtoms * nb; i += 32) {
+        const uint32_t dst = s_base + st * kStageBytes;
+        for (int i = lane; i < (kAtoms + 1) * nb; i += 32) {
           const int at = i / nb;
-          tma_load_2d(dst + at * kAtomBytes, &tc, at < 4 ? (int)rank * kHalf + at * 64 : kLatentDim, row,
-                      bar(kKFull + st));
+          if (at < kAtoms)
+            tma_load_2d(dst + at * kAtomBytes + b * a.block_size * 128, &tc, (int)rank * kHalf + at * 64, row,
+                        bar(kKFull + st));
+          else
+            tma_load_2d(dst + kAtoms * kAtomBytes + b * a.block_size * 64, &tr,
+                        kLatentDim + (int)rank * (kRopeDim / 2), row, bar(kKFull + st));
         }
         row = tile_row(t + 1);
       }
@@ -383,47 +393,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
     constexpr uint32_t kIdPV = umma_idesc_f16(kRows, kHalf, false, true);
     const uint64_t k_desc = umma_desc_sw128(s_base, 16, 1024);
+    const uint64_t r_desc = umma_desc_sw64(s_base + kAtoms * kAtomBytes, 512);
     const uint64_t v_desc = umma_desc_sw128(s_base, kAtomBytes, 1024);
+    const uint64_t p_desc = umma_desc_sw128(s_base + kOffP, 16, 1024);
     constexpr uint64_t kStep = (uint64_t)kStageBytes >> 4;
-    int i = 0, j = 0, seg = 0, t = 0;
+    int i = 0, j = 0, seg = 0, t = 0, t_end = 0, live_end = 0;
     unsigned firsts = 0;  // bit j % 32: tile j starts a segment
-    w.t_end = 0;
     bool ok = true;
-    uint64_t t0 = global_timer_ns();
+    uint64_t t0 = 0;
     unsigned polls = 0;
     while (j < n_tiles) {
-      // 2: P.V(j) can start; 1: S(i) can.  P.V first: the next tile's P waits
-      // for it.
-      int r = 0;
-      if (j < i && mbar_test(bar(kPFull), j & 1))
-        r = 2;
-      else if (i < n_tiles && (i == 0 || mbar_test(bar(kSFree), (i - 1) & 1)) &&
-               mbar_test(bar(kKFull + i % kStages), (i / kStages) & 1) &&
-               (t < w.t_end || mbar_test(bar(kQFull), seg & 1)))
-        r = 1;
-      else if ((++polls & 255) == 0 && (global_timer_ns() - t0 > kWaitLimitNs || *fail))
-        r = 3;
-      r = __shfl_sync(kFullMask, r, 0);
-      if (r == 0) continue;
-      if (r == 3) {
-        ok = false;
-        break;
-      }
-      // Every lane has seen the phases that lane 0 saw (they are complete).
-      if (r == 1) {
-        const int st = i % kStages;
-        mbar_wait_bounded(bar(kKFull + st), (i / kStages) & 1);
-        if (t >= w.t_end) {
-          w.next(a);
-          t = w.t_begin;
-          firsts |= 1u << (i % 32);
-          ++seg;
-        } else {
-          firsts &= ~(1u << (i % 32));
+      // P.V(j) can start, or S(i) can.  P.V first: it frees a stage and the
+      // next P's place.  Votes, not shuffles: the compiler takes their results
+      // for uniform, and with them the descriptors.
+      const bool do_pv = j < i && __any_sync(kFullMask, mbar_test(bar(kPFull + (j & 1)), (j >> 1) & 1));
+      const bool do_qk = !do_pv && i < n_tiles &&
+                         __any_sync(kFullMask, i == 0 || mbar_test(bar(kSFree), (i - 1) & 1)) &&
+                         __any_sync(kFullMask, mbar_test(bar(kKFull + i % kStages), (i / kStages) & 1)) &&
+                         (t < t_end || __any_sync(kFullMask, mbar_test(bar(kQFull), seg & 1)));
+      if (!do_pv && !do_qk) {
+        // The timer is read now and then only: it takes as long as a product.
+        if ((++polls & 1023) == 0) {
+          const uint64_t now = global_timer_ns();
+          if (polls == 1024) t0 = now;
+          if (__any_sync(kFullMask, now - t0 > kWaitLimitNs || *fail)) {
+            ok = false;
+            break;
+          }
         }
+        continue;
+      }
+      polls = 0;
+      if (do_qk) {
+        const int st = i % kStages;
+        // Every lane sees the phase that one lane saw (it is complete).
+        mbar_wait_bounded(bar(kKFull + st), (i / kStages) & 1);
+        const bool first = t >= t_end;
+        if (first) {
+          w.next(a);
+          t = __shfl_sync(kFullMask, w.t_begin, 0);
+          t_end = __shfl_sync(kFullMask, w.t_end, 0);
+          live_end = __shfl_sync(kFullMask, w.c, 0);
+          ++seg;
+        }
+        firsts = (firsts & ~(1u << (i % 32))) | (unsigned)first << (i % 32);
         // Rows past the context: stale slots may hold anything, and 0 * NaN
         // would poison O (their logits are masked).
-        const int live = w.c - t * kTile;
+        const int live = live_end - t * kTile;
         if (live < kTile) {
           unsigned char* v = sm + st * kStageBytes;
           const int chunks = (kTile - live) * 8;
@@ -444,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             umma_f16_tmem_a(tmem + kColS, tmem + kColQ + 128 + 8 * k,
-                            kd + (uint64_t)((4 * kAtomBytes + k * 32) >> 4) + (uint64_t)(rank * 4), kIdQK, true);
+                            r_desc + st * kStep + (uint64_t)((k * 32) >> 4), kIdQK, true);
           umma_commit(bar(kSFull + (i & 1)));
         }
         __syncwarp();
@@ -456,17 +472,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint64_t vd = v_desc + st * kStep;
         if (elect_one()) {
+          if (j & 1) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            umma_f16_tmem_a(tmem, tmem + kColP + 8 * k, vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV,
-                            !first || k > 0);
+            for (int k = 0; k < kTile / 16; ++k)
+              umma_f16(tmem, p_desc + (uint64_t)((k * 32) >> 4), vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV,
+                       !first || k > 0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              umma_f16_tmem_a(tmem, tmem + kColP + 8 * k, vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV,
+                              !first || k > 0);
+          }
           umma_commit(bar(kKEmpty + st));
           umma_commit(bar(kOFull + (j & 1)));
         }
         __syncwarp();
         ++j;
       }
-      t0 = global_timer_ns();
     }
     if (!ok && lane == 0) {
       atomicOr(a.err, PA_ERRBIT_TIMEOUT);
@@ -611,15 +633,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_arrive(bar(kRef + x));
         }
-        // P and O are free once P.V of the tile before is done (a segment's
-        // epilogue has waited for its last).
-        if (!first) {
-          ok = all(mbar_wait_bounded(bar(kOFull + (x ^ 1)), ((g - 1) >> 1) & 1));
-          if (!ok) break;
-        }
+        // This group's P is free once P.V of its tile before is done; O may be
+        // rescaled once that of the other group's is, too.
+        ok = g < 2 || all(mbar_wait_bounded(bar(kOFull + x), par ^ 1));
+        if (!ok) break;
         if (live) {
           tc_fence_after();
           if (!first && rescale) {
+            ok = all(mbar_wait_bounded(bar(kOFull + (x ^ 1)), ((g - 1) >> 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1  // seldom taken: unrolled, it costs the loop its registers
             for (int cb = 0; cb < kHalf / 32; ++cb) {
               uint32_t r[32];
@@ -630,11 +653,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st32(tmem + t_lane + cb * 32, r);
             }
           }
-          tmem_st32(tmem + t_lane + kColP, pk);
-          tmem_wait_st();
+          if (x == 0) {
+            tmem_st32(tmem + t_lane + kColP, pk);
+          } else {
+            unsigned char* p_row = sm + kOffP + row * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4*>(p_row + ((c ^ (row & 7)) << 4)) =
+                  make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+            fence_proxy_async_smem();
+          }
+          tmem_wait_st();  // P, or the rescaled output
           tc_fence_before();
         }
-        mbar_arrive(bar(kPFull));
+        mbar_arrive(bar(kPFull + x));
       }
       if (!ok) break;
       g = g_end;
@@ -907,11 +939,14 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
   }
   const LatentLayout l = latent_layout(g.num_seqs, g.num_heads, g.sms);
   const long long rows = (long long)g.num_blocks * g.block_size;
-  CUtensorMap tc;
+  CUtensorMap tc, tr;
   const cuuint64_t str[1] = {(cuuint64_t)kLatentRow * 2};
   const cuuint64_t cdims[2] = {(cuuint64_t)kLatentRow, (cuuint64_t)rows};
   const cuuint32_t cbox[2] = {64, (cuuint32_t)g.block_size};
-  if (!encode_tensor_map(&tc, g.cache, 2, cdims, str, cbox)) return cudaErrorInvalidValue;
+  const cuuint32_t rbox[2] = {kRopeDim / 2, (cuuint32_t)g.block_size};
+  if (!encode_tensor_map(&tc, g.cache, 2, cdims, str, cbox) ||
+      !encode_tensor_map(&tr, g.cache, 2, cdims, str, rbox, false, CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
   LatentParams p{};
   p.out = g.out;
   p.query = g.query;
@@ -934,7 +969,7 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
     p.seq_begin = b;
     p.num_seqs = g.num_seqs - b < kSeqsPerLaunch ? g.num_seqs - b : kSeqsPerLaunch;
     e = launch_pdl_cluster(latent_decode_kernel, dim3((unsigned)(2 * l.workers * l.head_tiles)),
-                           dim3(kThreads), 2, kSmem, stream, tc, p);
+                           dim3(kThreads), 2, kSmem, stream, tc, tr, p);
     if (e != cudaSuccess) return e;
     const long long pairs = (long long)p.num_seqs * p.num_heads;
     e = p.num_seqs < l.workers / 4

@@ -260,14 +260,19 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 }
 
 // Polls two barriers (for at most the bounded wait's time): true when the
-// second one's phase is complete and the first one's is not.  Warp-uniform.
+// second one's phase is complete and the first one's is not.  Votes make the
+// answer uniform for the compiler; the timer is read now and then only, since
+// that takes as long as a product.
 __device__ __forceinline__ bool second_first(uint32_t a, uint32_t a_parity, uint32_t b, uint32_t b_parity) {
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-    int r = mbar_test(a, a_parity) ? 1 : mbar_test(b, b_parity) ? 2 : 0;
-    if (r == 0 && global_timer_ns() - t0 > kWaitLimitNs) r = 1;  // the wait that follows reports it
-    r = __shfl_sync(kFullMask, r, 0);
-    if (r != 0) return r == 2;
+  uint64_t t0 = 0;
+  for (unsigned polls = 1;; ++polls) {
+    if (__any_sync(kFullMask, mbar_test(a, a_parity))) return false;
+    if (__any_sync(kFullMask, mbar_test(b, b_parity))) return true;
+    if ((polls & 1023) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (polls == 1024) t0 = now;
+      if (__any_sync(kFullMask, now - t0 > kWaitLimitNs)) return false;  // the wait that follows reports it
+    }
   }
 }
 

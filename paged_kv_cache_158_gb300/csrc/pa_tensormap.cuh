@@ -23,17 +23,18 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode_fn() {
   return fn;
 }
 
-// fp16 tensors with 128-byte swizzle (operand layout), or bytes unswizzled
-// (FP8 codes, widened in shared memory).
+// fp16 tensors with 128-byte swizzle (operand layout; or another), or bytes
+// unswizzled (FP8 codes, widened in shared memory).
 inline bool encode_tensor_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-            const cuuint64_t* strides, const cuuint32_t* box, bool bytes = false) {
+                              const cuuint64_t* strides, const cuuint32_t* box, bool bytes = false,
+                              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto fn = tensor_map_encode_fn();
   if (!fn) return false;
   const cuuint32_t es[3] = {1, 1, 1};
   return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
             (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE,
-            bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
