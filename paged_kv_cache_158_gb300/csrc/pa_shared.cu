@@ -23,14 +23,19 @@
 //    the tiles of all units are numbered in that order and cut into equal
 //    ranges, so few groups with long prefixes load every SM alike.  A worker's
 //    part of a unit is one segment; its rows go to partial rows
-//    H * s0 + h * rows + 128 * w (s0: the unit's first sequence; w: the
-//    worker), distinct because along the walk either the unit or w grows.
+//    4 H s0 + h * rows + 128 w (s0: the unit's first sequence; w: the worker;
+//    rows: the unit's, copies counted), distinct because along the walk either
+//    the unit or w grows.
 //  * Warps: four softmax warps (one query row a thread), TMA, MMA, and for
-//    E4M3 caches four that widen the codes to fp16 in shared memory (exact).
-//    The queries are the A operand from tensor memory, S is double-buffered
+//    E4M3 caches eight that widen the codes to fp16 in shared memory (exact).
+//    The queries are the A operand from tensor memory, S has four buffers
 //    there, P (fp16, rounded once) lies over the first half of its S, and the
-//    products of S(t + 1) and P.V(t) are issued in the order in which they
-//    become ready.
+//    products of S and P.V are issued in the order in which they become ready.
+//  * Copies: a tile's softmax takes a warp 0.7 us whatever the rows, and the
+//    products 128 rows whatever the members, so a unit of up to 32 (64) members
+//    has its queries in the lanes four (two) times and each copy's warps take
+//    every fourth (second) tile, their P being zero in the others.  Each copy
+//    keeps its own m, l and output rows, which the merge joins like segments.
 //  * Suffix: the decode's partition kernel from each sequence's first own
 //    position on.  It runs beside the prefix pass, which waits for its softmax
 //    more than for HBM: it reads nothing of it, so it starts as soon as the
@@ -54,6 +59,7 @@ namespace {
 
 constexpr int kRows = 128;    // query rows of a unit (MMA M)
 constexpr int kTile = 64;     // tokens of a tile
+constexpr int kBuffers = 4;   // of S
 constexpr int kPlanThreads = 1024;
 // Members below which a prefix is not worth a pass of its own.
 constexpr int kMinMembers = 2;
@@ -220,7 +226,7 @@ struct Traits {
   static constexpr int NA = D / 64;             // swizzle atoms per row
   static constexpr int ATOM = kTile * 128;      // kTile rows x 64 fp16
   static constexpr int TB = kTile * D * 2;      // one fp16 tile of K or V
-  static constexpr int NST = F8 ? 2 : 4;
+  static constexpr int NST = F8 ? 3 : 4;
   static constexpr int CB = kTile * D;          // one tile of codes
   static constexpr int NCS = F8 ? 4 : 0;        // stages of codes (K and V each)
   static constexpr int OFF_V = NST * TB;
@@ -229,21 +235,28 @@ struct Traits {
   static constexpr int USED = OFF_BAR + 512 + 1024;
   // At least 115 KB, so that two do not share an SM.
   static constexpr int SMEM = USED > 115 * 1024 ? USED : 115 * 1024;
-  static constexpr int THREADS = F8 ? 320 : 192;
-  static constexpr uint32_t COL_Q = 2 * kTile;  // S: kTile columns each
-  static constexpr uint32_t COL_O = COL_Q + 64; // Q: D / 2 columns; O: D columns
+  static constexpr int THREADS = F8 ? 448 : 192;
+  static constexpr uint32_t COL_Q = kBuffers * kTile;  // S: kTile columns each
+  static constexpr uint32_t COL_O = COL_Q + 2 * 64;    // Q: D / 2 columns, this segment's and the next's; O: D
   static_assert(COL_O + D <= 512, "tensor memory");
 };
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;  // base-2 logits above the reference that move it
 
-// Barriers.  S, P and O have one for each parity of the tile: their phases are
-// not all waited for, and S(g) only says that P.V(g - 2) is done, so a single
-// barrier's parity could be taken for the phase before.
+// Barriers.  S, P and O have one for each buffer of S (tile g mod 4): their
+// phases are not all waited for, and S(g) only says that P.V(g - 4) is done, so
+// a single barrier's parity could be taken for an earlier phase.
 enum {
-  kQFull = 0, kKFull = 1, kKEmpty = 5, kVFull = 9, kVEmpty = 13, kSFull = 17, kPFull = 19, kOFull = 21, kDone = 23,
-  kCFull = 24 /* K 4, V 4 */, kCEmpty = 32 /* K 4, V 4 */, kNumBars = 40
+  kQFull = 47 /* 2 */, kDone = 1, kDrain = 2, kKFull = 3, kKEmpty = 7, kVFull = 11, kVEmpty = 15, kSFull = 19, kPFull = 23,
+  kOFull = 27, kCFull = 31 /* K 4, V 4 */, kCEmpty = 39 /* K 4, V 4 */, kNumBars = 49
 };
+
+// Copies of a unit's rows in the 128 lanes.
+__device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 2 : 1; }
+// First partial row of a segment.
+__device__ __forceinline__ size_t partial_row(int H, int s0, int h, int rows, int copies, int worker) {
+  return (size_t)H * s0 * 4 + (size_t)h * rows * copies + (size_t)worker * kRows;
+}
 
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -257,23 +270,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
-}
-
-// Polls two barriers (for at most the bounded wait's time): true when the
-// second one's phase is complete and the first one's is not.  Votes make the
-// answer uniform for the compiler; the timer is read now and then only, since
-// that takes as long as a product.
-__device__ __forceinline__ bool second_first(uint32_t a, uint32_t a_parity, uint32_t b, uint32_t b_parity) {
-  uint64_t t0 = 0;
-  for (unsigned polls = 1;; ++polls) {
-    if (__any_sync(kFullMask, mbar_test(a, a_parity))) return false;
-    if (__any_sync(kFullMask, mbar_test(b, b_parity))) return true;
-    if ((polls & 1023) == 0) {
-      const uint64_t now = global_timer_ns();
-      if (polls == 1024) t0 = now;
-      if (__any_sync(kFullMask, now - t0 > kWaitLimitNs)) return false;  // the wait that follows reports it
-    }
-  }
 }
 
 // Widens one tile of codes (row-major) into the swizzled fp16 operand layout:
@@ -312,11 +308,11 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 160) {
     for (int i = 0; i < kNumBars; ++i) {
-      const bool by_wideners = F8 && ((i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) || i >= kCEmpty);
-      mbar_init(bar(i), i == kQFull || i == kPFull || i == kPFull + 1 ? 128
-                        : i == kDone                                  ? T::THREADS
-                        : by_wideners                                 ? 4
-                                                                      : 1);
+      const bool by_wideners = F8 && ((i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) || (i >= kCEmpty && i < kQFull));
+      mbar_init(bar(i), i >= kQFull || (i >= kPFull && i < kOFull) ? 128
+                        : i == kDone                               ? T::THREADS
+                        : by_wideners                              ? 4
+                                                                   : 1);
     }
     *fail = 0;
     fence_mbar_init();
@@ -332,13 +328,15 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(kFullMask, *tmem_slot, 0);
   const int worker = blockIdx.x;
   Walk w;
+  int n_tiles;
   {
     const int total = *a.total, W = active_workers(a, total);
     w.tile = worker < W ? worker_begin(worker, W, total) : 0;
     w.left = worker < W ? worker_begin(worker + 1, W, total) - w.tile : 0;
+    n_tiles = w.left;
     // The last group that starts at or before the tile and has any.
     int lo = 0, hi = a.num_groups - 1;
     while (lo < hi) {
@@ -415,174 +413,195 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
         mbar_wait_bounded(bar((F8 ? kCFull + 4 : kVFull) + u % N), (u / N) & 1);
     }
   } else if (warp == 5) {
-    // ---------------- MMA
-    constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
-    constexpr uint32_t kIdPV = umma_idesc_f16(kRows, D, false, true);
-    const uint64_t k_desc = umma_desc_sw128(s_base, 16, 1024);
-    const uint64_t v_desc = umma_desc_sw128(s_base + T::OFF_V, T::ATOM, 1024);
-    constexpr uint64_t kStep = (uint64_t)T::TB >> 4;
-    auto uni = [&](bool v) { return __all_sync(kFullMask, v); };
-    int qk = 0, pv = 0;
-    // P.V of tile g; `first`: it starts a segment.
-    auto pv_mma = [&](int g, bool first) {
-      bool ok = uni(mbar_wait_bounded(bar(kPFull + (g & 1)), (g >> 1) & 1));
-      ok = ok && uni(mbar_wait_bounded(bar(kVFull + g % NST), (g / NST) & 1));
-      if (!ok) return false;
-      tc_fence_after();
-      const uint64_t vd = v_desc + (g % NST) * kStep;
-      if (elect_one()) {
+    // ---------------- MMA: S of tile i or P.V of tile j, whichever can start.
+    // One thread does all of it: a vote or a warp-wide branch at each step costs
+    // more than the step's products.
+    if (elect_one()) {
+      constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
+      constexpr uint32_t kIdPV = umma_idesc_f16(kRows, D, false, true);
+      const uint64_t k_desc = umma_desc_sw128(s_base, 16, 1024);
+      const uint64_t v_desc = umma_desc_sw128(s_base + T::OFF_V, T::ATOM, 1024);
+      constexpr uint64_t kStep = (uint64_t)T::TB >> 4;
+      int i = 0, j = 0, seg = -1, left = 0;  // left: tiles of i's segment still to come
+      unsigned firsts = 0;                   // bit j % 32: tile j starts a segment
+      uint64_t t0 = 0;
+      unsigned polls = 0;
+      while (j < n_tiles) {
+        if (j < i && mbar_test(bar(kPFull + (j & 3)), (j >> 2) & 1) &&
+            mbar_test(bar(kVFull + j % NST), (j / NST) & 1)) {
+          // P.V first: it frees a stage and a buffer of S.
+          tc_fence_after();
+          const bool first = firsts >> (j % 32) & 1;
+          const uint64_t vd = v_desc + (j % NST) * kStep;
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          umma_f16_tmem_a(tmem + T::COL_O, tmem + kTile * (g & 1) + 8 * k,
-                          vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV, !first || k > 0);
-        umma_commit(bar(kVEmpty + g % NST));
-        umma_commit(bar(kOFull + (g & 1)));
-      }
-      __syncwarp();
-      ++pv;
-      return true;
-    };
-    int g = 0, seg = 0;
-    bool ok = true, prev_first = false;
-    while (ok && w.next(a)) {
-      // The next queries come after the last segment's output, so its last P.V
-      // goes first.
-      if (pv < g) ok = pv_mma(g - 1, prev_first);
-      ok = ok && uni(mbar_wait_bounded(bar(kQFull), seg & 1));
-      for (int t = w.t_begin; ok && t < w.t_end; ++t, ++g) {
-        const int st = g % NST;
-        // Of S(t) and P.V of the tile before, the one that can start first.
-        if (pv < g && second_first(bar(kKFull + st), (g / NST) & 1, bar(kPFull + ((g - 1) & 1)), ((g - 1) >> 1) & 1))
-          ok = pv_mma(g - 1, prev_first);
-        ok = ok && uni(mbar_wait_bounded(bar(kKFull + st), (g / NST) & 1));
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t kd = k_desc + st * kStep;
-        if (elect_one()) {
+          for (int k = 0; k < kTile / 16; ++k)
+            umma_f16_tmem_a(tmem + T::COL_O, tmem + kTile * (j & 3) + 8 * k,
+                            vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV, !first || k > 0);
+          umma_commit(bar(kVEmpty + j % NST));
+          umma_commit(bar(kOFull + (j & 3)));
+          ++j;
+          polls = 0;
+        } else if (i < n_tiles && i < j + kBuffers && mbar_test(bar(kKFull + i % NST), (i / NST) & 1) &&
+                   (left > 0 || mbar_test(bar(kQFull + ((seg + 1) & 1)), ((seg + 1) >> 1) & 1))) {
+          tc_fence_after();
+          const bool first = left == 0;
+          if (first) {
+            w.next(a);
+            left = w.t_end - w.t_begin;
+            ++seg;
+          }
+          firsts = (firsts & ~(1u << (i % 32))) | (unsigned)first << (i % 32);
+          --left;
+          const uint64_t kd = k_desc + (i % NST) * kStep;
+          const uint32_t qa = tmem + T::COL_Q + 64 * (seg & 1);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint64_t off = (uint64_t)(((k / 4) * T::ATOM + (k % 4) * 32) >> 4);
-            umma_f16_tmem_a(tmem + kTile * (g & 1), tmem + T::COL_Q + 8 * k, kd + off, kIdQK, k > 0);
+            umma_f16_tmem_a(tmem + kTile * (i & 3), qa + 8 * k, kd + off, kIdQK, k > 0);
           }
-          umma_commit(bar(kSFull + (g & 1)));
-          umma_commit(bar(kKEmpty + st));
+          umma_commit(bar(kSFull + (i & 3)));
+          umma_commit(bar(kKEmpty + i % NST));
+          ++i;
+          polls = 0;
+        } else if ((++polls & 1023) == 0) {
+          // The timer is read now and then only: it takes as long as a product.
+          const uint64_t now = global_timer_ns();
+          if (polls == 1024) t0 = now;
+          if (now - t0 > kWaitLimitNs || *fail) {
+            atomicOr(a.err, PA_ERRBIT_TIMEOUT);
+            *fail = 1;
+            // Every product started ends (bounded) before its memory goes.
+            umma_commit(bar(kDrain));
+            mbar_wait_bounded(bar(kDrain), 0);
+            break;
+          }
         }
-        __syncwarp();
-        ++qk;
-        if (pv < g) ok = pv_mma(g - 1, prev_first);
-        prev_first = t == w.t_begin;
       }
-      ++seg;
     }
-    if (ok && g > 0) ok = pv_mma(g - 1, prev_first);
-    if (!ok && lane == 0) {
-      atomicOr(a.err, PA_ERRBIT_TIMEOUT);
-      *fail = 1;
-      // Every product started ends (bounded) before its memory goes.
-      if (qk > 0) mbar_wait_bounded(bar(kSFull + ((qk - 1) & 1)), ((qk - 1) >> 1) & 1);
-      if (pv > 0) mbar_wait_bounded(bar(kOFull + ((pv - 1) & 1)), ((pv - 1) >> 1) & 1);
-    }
+    __syncwarp();
   } else if (warp < 4) {
-    // ---------------- softmax: one query row a thread
+    // ---------------- softmax: one query row (of one copy) a thread
     const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
-    const int row = tid;
-    int g = 0;
+    const bool neg = a.scale_log2 < 0.f;  // then the largest logit is the smallest product
+    const float scale = fabsf(a.scale_log2);
+    const uint64_t scale2 = f32x2_splat(scale);
+    auto all = [&](bool v) { return __all_sync(kFullMask, v && !*fail); };
+    int g = 0, seg = 0;
     bool ok = true;
-    while (ok && w.next(a)) {
-      const bool live = warp * 32 < w.rows;  // this warp has members
-      // The queries to tensor memory (the last segment's Q K^T products are
-      // done: their S has been read).  Rows past the members are zero.
-      if (live) {
+    // The queries of a segment to tensor memory, a segment ahead (the place was
+    // the one before the last segment's, whose S has been read).  Rows past the
+    // members are zero.
+    auto load_queries = [&](const Walk& n, int buffer) {
+      const int warps = 4 / copies_of(n.rows);
+      const int row = (warp % warps) * 32 + lane;
+      if ((row & ~31) < n.rows) {
         const uint4* q = reinterpret_cast<const uint4*>(
-            static_cast<const __half*>(a.query) + ((size_t)(w.s0 + (row < w.rows ? row : 0)) * a.num_heads + w.h) * D);
+            static_cast<const __half*>(a.query) + ((size_t)(n.s0 + (row < n.rows ? row : 0)) * a.num_heads + n.h) * D);
 #pragma unroll
         for (int cb = 0; cb < T::NA; ++cb) {
           uint32_t r[32];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const uint4 v = row < w.rows ? q[cb * 8 + c] : make_uint4(0, 0, 0, 0);
+            const uint4 v = row < n.rows ? q[cb * 8 + c] : make_uint4(0, 0, 0, 0);
             r[4 * c] = v.x;
             r[4 * c + 1] = v.y;
             r[4 * c + 2] = v.z;
             r[4 * c + 3] = v.w;
           }
-          tmem_st32(tmem + t_lane + T::COL_Q + 32 * cb, r);
+          tmem_st32(tmem + t_lane + T::COL_Q + 64 * buffer + 32 * cb, r);
         }
         tmem_wait_st();
         tc_fence_before();
       }
-      mbar_arrive(bar(kQFull));
+      mbar_arrive(bar(kQFull + buffer));
+    };
+    Walk ahead = w;
+    bool more = ahead.next(a);
+    if (more) load_queries(ahead, 0);
+    while (ok && more) {
+      w = ahead;
+      more = ahead.next(a);
+      if (more) load_queries(ahead, (seg + 1) & 1);
+      ++seg;
+      const int copies = copies_of(w.rows), warps = 4 / copies;  // warps of a copy
+      const int copy = warp / warps;
+      const int row = (warp - copy * warps) * 32 + lane;
+      const bool live = (row & ~31) < w.rows;  // this warp has members
       float m = -INFINITY, l = 0.f;
       for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
-        const uint32_t t_s = tmem + t_lane + kTile * (g & 1);
-        ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kSFull + (g & 1)), (g >> 1) & 1) && !*fail);
+        const uint32_t t_s = tmem + t_lane + kTile * (g & 3);
+        ok = all(mbar_wait_bounded(bar(kSFull + (g & 3)), (g >> 2) & 1));
         if (!ok) break;
         if (live) {
           tc_fence_after();
-          float x[kTile];
-          {
-            uint32_t sr[kTile];
-#pragma unroll
-            for (int cb = 0; cb < kTile / 32; ++cb)
-              tmem_ld32(t_s + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cb * 32]));
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < kTile; ++j) x[j] = __uint_as_float(sr[j]) * a.scale_log2;
-          }
-          const int lim = w.prefix - t * kTile;  // the prefix may end inside the tile
-          if (lim < kTile) {
-#pragma unroll
-            for (int j = 0; j < kTile; ++j)
-              if (j >= lim) x[j] = -INFINITY;
-          }
-          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < kTile; j += 8)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) mq[u] = fmax3(mq[u], x[j + 2 * u], x[j + 2 * u + 1]);
-          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-          float alpha = 1.f;
-          if (mx > m + kRescale || m == -INFINITY) {
-            alpha = m == -INFINITY ? 1.f : exp2_approx(m - mx);
-            m = mx;
-          }
-          const float ref = m == -INFINITY ? 0.f : m;
           uint32_t pk[kTile / 2];
-          float sq[4] = {0.f, 0.f, 0.f, 0.f};
+          if ((t - w.t_begin) % copies == copy) {
+            float x[kTile];
+            tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+            tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+            tmem_wait_ld();
+            if (neg) {
 #pragma unroll
-          for (int j = 0; j < kTile / 2; ++j) {
-            pk[j] = exp2_f32_to_f16x2(x[2 * j] - ref, x[2 * j + 1] - ref);
-            sq[j & 3] = add_f16x2_f32(pk[j], sq[j & 3]);
-          }
-          l = l * alpha + ((sq[0] + sq[1]) + (sq[2] + sq[3]));
-          if (t > w.t_begin && __any_sync(kFullMask, alpha != 1.f)) {
-            // O holds the tiles up to t - 1 once P.V of t - 1 is done.
-            ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kOFull + ((g - 1) & 1)), ((g - 1) >> 1) & 1) && !*fail);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int cb = 0; cb < D / 32; ++cb) {
-              uint32_t r[32];
-              tmem_ld32(tmem + t_lane + T::COL_O + cb * 32, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-              tmem_st32(tmem + t_lane + T::COL_O + cb * 32, r);
+              for (int j = 0; j < kTile; ++j) x[j] = -x[j];
             }
+            const int lim = w.prefix - t * kTile;  // the prefix may end inside the tile
+            if (lim < kTile) {
+#pragma unroll
+              for (int j = 0; j < kTile; ++j)
+                if (j >= lim) x[j] = -INFINITY;
+            }
+            float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < kTile; j += 8)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) mq[u] = fmax3(mq[u], x[j + 2 * u], x[j + 2 * u + 1]);
+            const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * scale;
+            float alpha = 1.f;
+            if (mx > m + kRescale || m == -INFINITY) {
+              alpha = m == -INFINITY ? 1.f : exp2_approx(m - mx);
+              m = mx;
+            }
+            const uint64_t neg2 = f32x2_splat(m == -INFINITY ? 0.f : -m);
+            float sq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < kTile / 2; ++j) {
+              const float2 e = ffma2(x[2 * j], x[2 * j + 1], scale2, neg2);
+              pk[j] = exp2_f32_to_f16x2(e.x, e.y);
+              sq[j & 3] = add_f16x2_f32(pk[j], sq[j & 3]);
+            }
+            l = l * alpha + ((sq[0] + sq[1]) + (sq[2] + sq[3]));
+            if (t > w.t_begin && __any_sync(kFullMask, alpha != 1.f)) {
+              // O holds the tiles up to t - 1 once P.V of t - 1 is done.
+              ok = all(mbar_wait_bounded(bar(kOFull + ((g - 1) & 3)), ((g - 1) >> 2) & 1));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int cb = 0; cb < D / 32; ++cb) {
+                uint32_t r[32];
+                tmem_ld32(tmem + t_lane + T::COL_O + cb * 32, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+                tmem_st32(tmem + t_lane + T::COL_O + cb * 32, r);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kTile / 2; ++j) pk[j] = 0;  // another copy's tile
           }
           tmem_st32(t_s, pk);  // P over the first half of its S
           tmem_wait_st();
           tc_fence_before();
         }
-        mbar_arrive(bar(kPFull + (g & 1)));
+        mbar_arrive(bar(kPFull + (g & 3)));
       }
       if (!ok) break;
       // The segment's partial rows.
-      ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kOFull + ((g - 1) & 1)), ((g - 1) >> 1) & 1) && !*fail);
+      ok = all(mbar_wait_bounded(bar(kOFull + ((g - 1) & 3)), ((g - 1) >> 2) & 1));
       if (!ok) break;
       if (live) {
         tc_fence_after();
-        const size_t pr = (size_t)a.num_heads * w.s0 + (size_t)w.h * w.rows + (size_t)worker * kRows + row;
+        const size_t pr = partial_row(a.num_heads, w.s0, w.h, w.rows, copies, worker) + copy * w.rows + row;
         if (row < w.rows) a.pre_ml[pr] = make_float2(m, l);
 #pragma unroll
         for (int cb = 0; cb < D / 32; ++cb) {
@@ -603,26 +622,25 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
     }
     if (!ok && lane == 0) *fail = 1;
   } else if constexpr (F8) {
-    // ---------------- E4M3 caches: four warps widen the staged codes
-    const int i = tid - 192;
+    // ---------------- E4M3 caches: four warps widen the staged codes of K, four
+    // those of V (apart, so that a V stage still in use does not hold back the
+    // next K; with two and two a tile took them 0.6 us, half of it latency)
+    const int kv = (warp - 6) >> 2, i = (tid - 192) & 127;
     int g = 0;
     bool ok = true;
     while (ok && w.next(a)) {
-      for (int t = w.t_begin; ok && t < w.t_end; ++t, ++g) {
+      for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
         const int cs = g % NCS, st = g % NST;
-#pragma unroll
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          ok = mbar_wait_bounded(bar(kCFull + 4 * kv + cs), (g / NCS) & 1);
-          if (g >= NST) ok = ok && mbar_wait_bounded(bar((kv ? kVEmpty : kKEmpty) + st), (g / NST - 1) & 1);
-          ok = __all_sync(kFullMask, ok && !*fail);
-          if (!ok) break;
-          widen<D>(sm + T::OFF_C + (NCS * kv + cs) * T::CB, sm + (kv ? T::OFF_V : 0) + st * T::TB, i);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(kCEmpty + 4 * kv + cs));
-            mbar_arrive(bar((kv ? kVFull : kKFull) + st));
-          }
+        ok = mbar_wait_bounded(bar(kCFull + 4 * kv + cs), (g / NCS) & 1);
+        if (g >= NST) ok = ok && mbar_wait_bounded(bar((kv ? kVEmpty : kKEmpty) + st), (g / NST - 1) & 1);
+        ok = __all_sync(kFullMask, ok && !*fail);
+        if (!ok) break;
+        widen<D>(sm + T::OFF_C + (NCS * kv + cs) * T::CB, sm + (kv ? T::OFF_V : 0) + st * T::TB, i);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kCEmpty + 4 * kv + cs));
+          mbar_arrive(bar((kv ? kVFull : kKFull) + st));
         }
       }
     }
@@ -653,22 +671,25 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams a)
   const int s = (int)(pair / a.num_heads), h = (int)(pair - (long long)s * a.num_heads);
   const int c = context_of(a, s), start = a.seq_start[s], g = a.seq_group[s];
   const int n_suf = c > start ? (c - start + a.part_tokens - 1) / a.part_tokens : 0;
-  int n_pre = 0;
+  int n_pre = 0, copies = 1, rows = 0;
   size_t pre0 = 0;
   if (g >= 0) {
     const GroupPlan p = a.groups[g];
     const int total = *a.total, W = active_workers(a, total);
     const int mt = (s - p.s_begin) / kRows, s0 = p.s_begin + mt * kRows;
-    const int rows = min(kRows, p.s_end - s0);
+    rows = min(kRows, p.s_end - s0);
+    copies = copies_of(rows);
     const int t0 = p.tile_base + (mt * a.num_heads + h) * p.tiles;
     const int w0 = worker_of(t0, W, total), w1 = worker_of(t0 + p.tiles - 1, W, total);
-    n_pre = w1 - w0 + 1;
-    pre0 = (size_t)a.num_heads * s0 + (size_t)h * rows + (size_t)w0 * kRows + (s - s0);
+    n_pre = (w1 - w0 + 1) * copies;
+    pre0 = partial_row(a.num_heads, s0, h, rows, copies, w0) + (s - s0);
   }
   const int n = n_pre + n_suf;
   const size_t suf0 = (size_t)pair * a.max_parts;
+  // Partial i of the prefix: segment i / copies, copy i % copies.
+  auto pre_row = [&](int i) { return pre0 + (size_t)(i / copies) * kRows + (i % copies) * rows; };
   auto ml_of = [&](int i) {
-    return i < n_pre ? a.pre_ml[pre0 + (size_t)i * kRows]
+    return i < n_pre ? a.pre_ml[pre_row(i)]
                      : reinterpret_cast<const float2*>(a.suf_ml)[suf0 + (i - n_pre)];
   };
   float M = -INFINITY;
@@ -692,7 +713,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams a)
 #pragma unroll 4
     for (int j = 0; j < cnt; ++j) {
       const int i = base + j;
-      const float* src = (i < n_pre ? a.pre_o + (pre0 + (size_t)i * kRows) * D
+      const float* src = (i < n_pre ? a.pre_o + pre_row(i) * D
                                     : a.suf_o + (suf0 + (i - n_pre)) * D) + lane * N;
       const float x = __shfl_sync(kFullMask, wt, j);
       if constexpr (N == 4) {
@@ -722,7 +743,7 @@ struct Layout {
 Layout layout(int S, int G, int H, int D, int sms) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   Layout l{};
-  const size_t rows = (size_t)S * H + (size_t)sms * kRows;
+  const size_t rows = (size_t)S * H * 4 + (size_t)sms * kRows;
   l.total = 0;
   l.groups = 256;
   l.start = up(l.groups + (size_t)G * sizeof(GroupPlan));
