@@ -200,6 +200,11 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 WsLayout ws_layout(int S, int H, int D, int max_context_len, bool partials = false) {
   WsLayout w{};
   w.part_tokens = part_tokens_for(S, H, max_context_len);
+  // Behind a shared prefix the bound says little about the contexts' own parts,
+  // which are short as a rule: small partitions (128 sequences, 8192 + 1..512
+  // tokens: 122.5 us at 256, 125.2 at 512; 64 of 512 + 1..1536: 134.4, 135.4).
+  if (partials && w.part_tokens == 512 && g_part_override.load(std::memory_order_relaxed) == 0)
+    w.part_tokens = 256;
   w.max_parts = max_context_len > 0 ? (max_context_len + w.part_tokens - 1) / w.part_tokens : 1;
   w.launches = (S + pa::kMaxSeqsPerLaunch - 1) / pa::kMaxSeqsPerLaunch;
   if (w.launches < 1) w.launches = 1;

@@ -107,61 +107,95 @@ __device__ __forceinline__ int context_of(const SharedParams& a, int s) {
 
 // ---- plan -------------------------------------------------------------------
 
+// What bounds it is the chain of dependent loads, so lengths and bounds come to
+// shared memory together (batches that fit there: all but the largest).
+constexpr int kPlanSeqs = 4096, kPlanGroups = 1024;
+
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedParams a) {
   __shared__ long long sums[kPlanThreads / 32];
+  __shared__ int ctx_s[kPlanSeqs];
+  __shared__ int start_s[kPlanGroups + 1];
+  __shared__ int pre_s[kPlanGroups];    // blocks, then the shared tokens (0: none)
+  __shared__ int tiles_s[kPlanGroups];  // of all units
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int S = a.num_seqs, G = a.num_groups;
+  const bool seqs_here = S <= kPlanSeqs, groups_here = G <= kPlanGroups;
   pdl_wait();
   pdl_launch_dependents();
   for (int i = tid; i < a.num_counters; i += kPlanThreads) a.counters[i] = 0u;
-  for (int s = tid; s < a.num_seqs; s += kPlanThreads) {
-    a.seq_start[s] = 0;
-    a.seq_group[s] = -1;
-  }
-  // Bounds that do not increase would make groups overlap: nothing is shared.
+  if (seqs_here)
+    for (int s = tid; s < S; s += kPlanThreads) ctx_s[s] = context_of(a, s);
+  // Bounds that decrease would make groups overlap: nothing is shared.
   bool bad = false;
-  for (int g = tid; g < a.num_groups; g += kPlanThreads) {
-    const int b = a.group_start[g], e = a.group_start[g + 1];
-    bad |= b < 0 || b > e || e > a.num_seqs || a.prefix_blocks[g] < 0;
+  for (int g = tid; g < G; g += kPlanThreads) {
+    const int b = a.group_start[g], e = a.group_start[g + 1], p = a.prefix_blocks[g];
+    bad |= b < 0 || b > e || e > S || p < 0;
+    if (groups_here) {
+      start_s[g] = b;
+      pre_s[g] = p;
+      if (g == G - 1) start_s[G] = e;
+    }
   }
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(a.err, PA_ERRBIT_CONTEXT);
-  for (int g = warp; g < a.num_groups; g += kPlanThreads / 32) {
+  auto ctx = [&](int s) { return seqs_here ? ctx_s[s] : context_of(a, s); };
+  auto start = [&](int g) { return groups_here ? start_s[g] : a.group_start[g]; };
+  auto units = [&](const GroupPlan& p) { return (long long)((p.s_end - p.s_begin + kRows - 1) / kRows) * a.num_heads; };
+  for (int g = warp; g < G; g += kPlanThreads / 32) {
     GroupPlan p{};
     int blocks = 0, members = 0;
     if (!bad) {
-      p.s_begin = a.group_start[g];
-      p.s_end = a.group_start[g + 1];
-      blocks = min(a.prefix_blocks[g], a.max_prefix_blocks);
+      p.s_begin = start(g);
+      p.s_end = start(g + 1);
+      blocks = min(groups_here ? pre_s[g] : a.prefix_blocks[g], a.max_prefix_blocks);
     }
     p.prefix = blocks * a.block_size;
     p.leader = -1;
     if (blocks > 0)
       for (int s0 = p.s_begin; s0 < p.s_end; s0 += 32) {
         const int s = s0 + lane;
-        const unsigned in = __ballot_sync(kFullMask, s < p.s_end && context_of(a, s) >= p.prefix);
+        const unsigned in = __ballot_sync(kFullMask, s < p.s_end && ctx(s) >= p.prefix);
         if (in != 0 && p.leader < 0) p.leader = s0 + __ffs(in) - 1;
         members += __popc(in);
       }
-    if (members >= kMinMembers) {
-      p.tiles = (p.prefix + kTile - 1) / kTile;
-      for (int s = p.s_begin + lane; s < p.s_end; s += 32)
-        if (context_of(a, s) >= p.prefix) {
-          a.seq_start[s] = p.prefix;
-          a.seq_group[s] = g;
-        }
+    if (members >= kMinMembers) p.tiles = (p.prefix + kTile - 1) / kTile;
+    __syncwarp();  // every lane has read the group's blocks
+    if (lane == 0) {
+      a.groups[g] = p;
+      if (groups_here) {
+        pre_s[g] = p.tiles > 0 ? p.prefix : 0;
+        tiles_s[g] = (int)(p.tiles * units(p));
+      }
     }
-    if (lane == 0) a.groups[g] = p;
   }
   __syncthreads();
+  // First own position of every sequence: the last group that starts at or
+  // before it, if it is in that group and covers the prefix.
+  for (int s = tid; s < S; s += kPlanThreads) {
+    int first = 0, group = -1;
+    if (!bad && G > 0) {
+      int lo = 0, hi = G - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (start(mid) <= s) lo = mid; else hi = mid - 1;
+      }
+      if (start(lo) <= s && s < start(lo + 1)) {
+        const int pre = groups_here ? pre_s[lo] : a.groups[lo].tiles > 0 ? a.groups[lo].prefix : 0;
+        if (pre > 0 && ctx(s) >= pre) {
+          first = pre;
+          group = lo;
+        }
+      }
+    }
+    a.seq_start[s] = first;
+    a.seq_group[s] = group;
+  }
   // Running sum of the groups' tiles.
   long long carry = 0;
-  for (int base = 0; base < a.num_groups; base += kPlanThreads) {
+  for (int base = 0; base < G; base += kPlanThreads) {
     const int g = base + tid;
     long long n = 0;
-    if (g < a.num_groups) {
-      const GroupPlan p = a.groups[g];
-      n = (long long)p.tiles * ((p.s_end - p.s_begin + kRows - 1) / kRows) * a.num_heads;
-    }
+    if (g < G) n = groups_here ? tiles_s[g] : a.groups[g].tiles * units(a.groups[g]);
     long long x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -176,7 +210,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
       if (w < warp) before += sums[w];
       all += sums[w];
     }
-    if (g < a.num_groups) a.groups[g].tile_base = (int)(before + x - n);
+    if (g < G) a.groups[g].tile_base = (int)(before + x - n);
     carry += all;
   }
   if (tid == 0) *a.total = (int)carry;
@@ -663,12 +697,13 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
 template <int D>
 __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams a) {
   constexpr int N = D / 32;
-  pdl_wait();
-  pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const long long pair = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (pair >= (long long)a.num_seqs * a.num_heads) return;
+  long long pair = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const bool live = pair < (long long)a.num_seqs * a.num_heads;
+  if (!live) pair = 0;
   const int s = (int)(pair / a.num_heads), h = (int)(pair - (long long)s * a.num_heads);
+  // The lengths and the plan are read before the wait: the kernels before this
+  // one started after the plan had ended.
   const int c = context_of(a, s), start = a.seq_start[s], g = a.seq_group[s];
   const int n_suf = c > start ? (c - start + a.part_tokens - 1) / a.part_tokens : 0;
   int n_pre = 0, copies = 1, rows = 0;
@@ -684,6 +719,9 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams a)
     n_pre = (w1 - w0 + 1) * copies;
     pre0 = partial_row(a.num_heads, s0, h, rows, copies, w0) + (s - s0);
   }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!live) return;
   const int n = n_pre + n_suf;
   const size_t suf0 = (size_t)pair * a.max_parts;
   // Partial i of the prefix: segment i / copies, copy i % copies.
