@@ -127,7 +127,7 @@ constexpr float kRescale = 8.f;        // base-2 logits above the reference that
 enum {
   kKFull = 0 /* 4 */, kKEmpty = 4 /* 4 */, kQFull = 8, kSFull = 9 /* 2 */, kSFree = 11, kPFull = 12 /* 2 */,
   kOFull = 14 /* 2 */, kXFull = 16 /* 2 */, kXFree = 18 /* 2 */, kRef = 20 /* 2 */, kSegA = 22, kSegB = 23, kDone = 24,
-  kNumBars = 25
+  kDrain = 25, kNumBars = 26
 };
 
 struct LatentParams {
@@ -389,89 +389,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpMma) {
     // ---------------- MMA: S of tile i and P.V of tile j, whichever can start.
-    // S has one buffer (the softmax takes it to registers), P another.
-    constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
-    constexpr uint32_t kIdPV = umma_idesc_f16(kRows, kHalf, false, true);
-    const uint64_t k_desc = umma_desc_sw128(s_base, 16, 1024);
-    const uint64_t r_desc = umma_desc_sw64(s_base + kAtoms * kAtomBytes, 512);
-    const uint64_t v_desc = umma_desc_sw128(s_base, kAtomBytes, 1024);
-    const uint64_t p_desc = umma_desc_sw128(s_base + kOffP, 16, 1024);
-    constexpr uint64_t kStep = (uint64_t)kStageBytes >> 4;
-    int i = 0, j = 0, seg = 0, t = 0, t_end = 0, live_end = 0;
-    unsigned firsts = 0;  // bit j % 32: tile j starts a segment
-    bool ok = true;
-    uint64_t t0 = 0;
-    unsigned polls = 0;
-    while (j < n_tiles) {
-      // P.V(j) can start, or S(i) can.  P.V first: it frees a stage and the
-      // next P's place.  Votes, not shuffles: the compiler takes their results
-      // for uniform, and with them the descriptors.
-      const bool do_pv = j < i && __any_sync(kFullMask, mbar_test(bar(kPFull + (j & 1)), (j >> 1) & 1));
-      const bool do_qk = !do_pv && i < n_tiles &&
-                         __any_sync(kFullMask, i == 0 || mbar_test(bar(kSFree), (i - 1) & 1)) &&
-                         __any_sync(kFullMask, mbar_test(bar(kKFull + i % kStages), (i / kStages) & 1)) &&
-                         (t < t_end || __any_sync(kFullMask, mbar_test(bar(kQFull), seg & 1)));
-      if (!do_pv && !do_qk) {
-        // The timer is read now and then only: it takes as long as a product.
-        if ((++polls & 1023) == 0) {
-          const uint64_t now = global_timer_ns();
-          if (polls == 1024) t0 = now;
-          if (__any_sync(kFullMask, now - t0 > kWaitLimitNs || *fail)) {
-            ok = false;
-            break;
-          }
-        }
-        continue;
-      }
-      polls = 0;
-      if (do_qk) {
-        const int st = i % kStages;
-        // Every lane sees the phase that one lane saw (it is complete).
-        mbar_wait_bounded(bar(kKFull + st), (i / kStages) & 1);
-        const bool first = t >= t_end;
-        if (first) {
-          w.next(a);
-          t = __shfl_sync(kFullMask, w.t_begin, 0);
-          t_end = __shfl_sync(kFullMask, w.t_end, 0);
-          live_end = __shfl_sync(kFullMask, w.c, 0);
-          ++seg;
-        }
-        firsts = (firsts & ~(1u << (i % 32))) | (unsigned)first << (i % 32);
-        // Rows past the context: stale slots may hold anything, and 0 * NaN
-        // would poison O (their logits are masked).
-        const int live = live_end - t * kTile;
-        if (live < kTile) {
-          unsigned char* v = sm + st * kStageBytes;
-          const int chunks = (kTile - live) * 8;
-          for (int q = lane; q < chunks * kAtoms; q += 32) {
-            const int at = q / chunks, rr = live + (q % chunks) / 8, ch = q % 8;
-            *reinterpret_cast<uint4*>(v + at * kAtomBytes + rr * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        tc_fence_after();
-        const uint64_t kd = k_desc + st * kStep;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            umma_f16_tmem_a(tmem + kColS, tmem + kColQ + 8 * k,
-                            kd + (uint64_t)(((k / 4) * kAtomBytes + (k % 4) * 32) >> 4), kIdQK, k > 0);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            umma_f16_tmem_a(tmem + kColS, tmem + kColQ + 128 + 8 * k,
-                            r_desc + st * kStep + (uint64_t)((k * 32) >> 4), kIdQK, true);
-          umma_commit(bar(kSFull + (i & 1)));
-        }
-        __syncwarp();
-        ++i;
-        ++t;
-      } else {
-        const int st = j % kStages;
-        const bool first = firsts >> (j % 32) & 1;
-        tc_fence_after();
-        const uint64_t vd = v_desc + st * kStep;
-        if (elect_one()) {
+    // S has one buffer (the softmax takes it to registers), P two.  One thread
+    // does all of it: a vote or a warp-wide branch at each step costs more than
+    // the step's products.
+    if (elect_one()) {
+      constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
+      constexpr uint32_t kIdPV = umma_idesc_f16(kRows, kHalf, false, true);
+      const uint64_t k_desc = umma_desc_sw128(s_base, 16, 1024);
+      const uint64_t r_desc = umma_desc_sw64(s_base + kAtoms * kAtomBytes, 512);
+      const uint64_t v_desc = umma_desc_sw128(s_base, kAtomBytes, 1024);
+      const uint64_t p_desc = umma_desc_sw128(s_base + kOffP, 16, 1024);
+      constexpr uint64_t kStep = (uint64_t)kStageBytes >> 4;
+      int i = 0, j = 0, seg = 0, left = 0;  // left: tiles of i's segment still to come
+      unsigned firsts = 0;                  // bit j % 32: tile j starts a segment
+      uint64_t t0 = 0;
+      unsigned polls = 0;
+      while (j < n_tiles) {
+        if (j < i && mbar_test(bar(kPFull + (j & 1)), (j >> 1) & 1)) {
+          // P.V first: it frees a stage and the next P's place.
+          const int st = j % kStages;
+          const bool first = firsts >> (j % 32) & 1;
+          tc_fence_after();
+          const uint64_t vd = v_desc + st * kStep;
           if (j & 1) {
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
@@ -485,18 +424,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           umma_commit(bar(kKEmpty + st));
           umma_commit(bar(kOFull + (j & 1)));
+          ++j;
+          polls = 0;
+        } else if (i < n_tiles && (i == 0 || mbar_test(bar(kSFree), (i - 1) & 1)) &&
+                   mbar_test(bar(kKFull + i % kStages), (i / kStages) & 1) &&
+                   (left > 0 || mbar_test(bar(kQFull), seg & 1))) {
+          const int st = i % kStages;
+          const bool first = left == 0;
+          if (first) {
+            w.next(a);
+            left = w.t_end - w.t_begin;
+            ++seg;
+          }
+          --left;
+          firsts = (firsts & ~(1u << (i % 32))) | (unsigned)first << (i % 32);
+          tc_fence_after();
+          const uint64_t kd = k_desc + st * kStep, rd = r_desc + st * kStep;
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            umma_f16_tmem_a(tmem + kColS, tmem + kColQ + 8 * k,
+                            kd + (uint64_t)(((k / 4) * kAtomBytes + (k % 4) * 32) >> 4), kIdQK, k > 0);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            umma_f16_tmem_a(tmem + kColS, tmem + kColQ + 128 + 8 * k, rd + (uint64_t)((k * 32) >> 4), kIdQK, true);
+          umma_commit(bar(kSFull + (i & 1)));
+          ++i;
+          polls = 0;
+        } else if ((++polls & 1023) == 0) {
+          // The timer is read now and then only: it takes as long as a product.
+          const uint64_t now = global_timer_ns();
+          if (polls == 1024) t0 = now;
+          if (now - t0 > kWaitLimitNs || *fail) {
+            atomicOr(a.err, PA_ERRBIT_TIMEOUT);
+            *fail = 1;
+            // Every product started ends (bounded) before its memory goes.
+            umma_commit(bar(kDrain));
+            mbar_wait_bounded(bar(kDrain), 0);
+            break;
+          }
         }
-        __syncwarp();
-        ++j;
       }
     }
-    if (!ok && lane == 0) {
-      atomicOr(a.err, PA_ERRBIT_TIMEOUT);
-      *fail = 1;
-      // Every product started ends (bounded) before its memory goes.
-      if (i > 0) mbar_wait_bounded(bar(kSFull + ((i - 1) & 1)), ((i - 1) >> 1) & 1);
-      if (j > 0) mbar_wait_bounded(bar(kOFull + ((j - 1) & 1)), ((j - 1) >> 1) & 1);
-    }
+    __syncwarp();
   } else {
     // ---------------- softmax: one head row a thread; warpgroup x takes the
     // tiles g = x mod 2
@@ -632,6 +601,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
           }
           mbar_arrive(bar(kRef + x));
+        }
+        // Rows past the context: stale slots may hold anything, and 0 * NaN would
+        // poison O (their logits were masked; Q K^T has read the tile).
+        {
+          const int left = w.c - t * kTile;
+          if (left < kTile) {
+            unsigned char* v = sm + (g % kStages) * kStageBytes;
+            const int chunks = (kTile - left) * 8;
+            for (int q = row; q < chunks * kAtoms; q += 128) {
+              const int at = q / chunks, rr = left + (q % chunks) / 8, ch = q % 8;
+              *reinterpret_cast<uint4*>(v + at * kAtomBytes + rr * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
         }
         // This group's P is free once P.V of its tile before is done; O may be
         // rescaled once that of the other group's is, too.
