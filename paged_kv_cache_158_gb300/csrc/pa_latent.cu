@@ -95,39 +95,39 @@ __global__ void __launch_bounds__(256)
 // ---- decode -----------------------------------------------------------------
 
 constexpr int kRows = 128;             // head rows of a cluster (MMA M)
-constexpr int kTile = 64;              // tokens of a tile
+constexpr int kTile = 32;              // tokens of a tile
 constexpr int kHalf = kLatentDim / 2;  // output values of a CTA
 constexpr int kAtoms = 4;              // its 64-value atoms of latent values
 constexpr int kAtomBytes = kTile * 128;
 constexpr int kRopeBytes = kTile * kRopeDim;  // its half of the rotary values
 constexpr int kStageBytes = kAtoms * kAtomBytes + kRopeBytes;
-constexpr int kStages = 4;
-constexpr int kThreads = 320;          // two softmax warpgroups, TMA, MMA
-constexpr int kWarpTma = 8, kWarpMma = 9;
+constexpr int kStages = 9;
+constexpr int kGroups = 3;             // softmax warpgroups
+constexpr int kThreads = 128 * kGroups + 64;
+constexpr int kWarpTma = 4 * kGroups, kWarpMma = kWarpTma + 1;
 constexpr int kSeqsPerLaunch = 1024;
 
 constexpr int kXBytes = kRows * kTile * 4;                 // one half of S from the other CTA
-constexpr int kOffX = kStages * kStageBytes;               // buffer b at kOffX + b * kXBytes
-constexpr int kOffP = kOffX + 2 * kXBytes;                 // P of odd tiles
-constexpr int kOffBar = kOffP + kRows * kTile * 2;
-constexpr int kOffRef = kOffBar + 256;                     // float [128]: each row's reference
-constexpr int kOffMl = kOffRef + kRows * 4;                // float2 [2][128]: reference and sum of each group
-constexpr int kSmem = kOffMl + 2 * kRows * 8;
+constexpr int kOffX = kStages * kStageBytes;               // group x's at kOffX + x * kXBytes
+constexpr int kOffBar = kOffX + kGroups * kXBytes;
+constexpr int kOffRef = kOffBar + 512;                     // float [128]: each row's reference
+constexpr int kOffMl = kOffRef + kRows * 4;                // float2 [groups][128]: reference and sum of each group
+constexpr int kSmem = kOffMl + kGroups * kRows * 8;
 static_assert(kSmem <= 232448, "beyond the opt-in shared memory of one CTA");
 
 constexpr uint32_t kTmemCols = 512;    // O: [0, 256)
-constexpr uint32_t kColQ = 256;        // queries: 128 columns latent, 16 rotary (and 16 unused)
-constexpr uint32_t kColS = 416;        // 64
-constexpr uint32_t kColP = 480;        // 32: P of even tiles (odd ones: shared memory, for want of columns)
+constexpr uint32_t kColQ = 256;        // queries: 128 columns latent, 16 rotary
+__device__ __forceinline__ uint32_t col_s(int g) { return 416 + 32 * (g & 1); }
+__device__ __forceinline__ uint32_t col_p(int x) { return x == 0 ? 400 : 464 + 16 * x; }  // 16 each
 
 constexpr float kRescale = 8.f;        // base-2 logits above the reference that move it
 
-// Barriers.  Those of two phases at a time that one warpgroup sees every
-// other one of come in pairs, by the tile's parity.
+// Barriers.  Those of S, P, O, the exchange and the reference are one for each
+// group (tile g mod 3): a group then sees every phase of the ones it waits for.
 enum {
-  kKFull = 0 /* 4 */, kKEmpty = 4 /* 4 */, kQFull = 8, kSFull = 9 /* 2 */, kSFree = 11, kPFull = 12 /* 2 */,
-  kOFull = 14 /* 2 */, kXFull = 16 /* 2 */, kXFree = 18 /* 2 */, kRef = 20 /* 2 */, kSegA = 22, kSegB = 23, kDone = 24,
-  kDrain = 25, kNumBars = 26
+  kKFull = 0 /* 9 */, kKEmpty = 9 /* 9 */, kQFull = 18, kSFull = 19 /* 3 */, kSFree = 22 /* 3 */, kPFull = 25 /* 3 */,
+  kOFull = 28 /* 3 */, kXFull = 31 /* 3 */, kXFree = 34 /* 3 */, kRef = 37 /* 3 */, kSegA = 40, kSegB = 41, kDone = 42,
+  kDrain = 43, kNumBars = 44
 };
 
 struct LatentParams {
@@ -275,11 +275,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int live_warps = min(4, (a.num_heads - h0 + 31) / 32);  // softmax warps with heads
   if (tid == kWarpMma * 32) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i == kSFree || i == kPFull || i == kPFull + 1 || i == kRef || i == kRef + 1 ? 128
-                        : i == kQFull || i == kSegA || i == kSegB                                    ? 256
-                        : i == kXFree || i == kXFree + 1                                             ? live_warps
-                        : i == kDone                                                                 ? kThreads
-                                                                                                     : 1);
+      mbar_init(bar(i), (i >= kSFree && i < kOFull) || (i >= kRef && i < kSegA) ? 128
+                        : i == kQFull || i == kSegA || i == kSegB               ? 128 * kGroups
+                        : i >= kXFree && i < kRef                               ? live_warps
+                        : i == kDone                                            ? kThreads
+                                                                                : 1);
     *fail = 0;
     fence_mbar_init();
     prefetch_tensormap(&tc);
@@ -347,22 +347,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && w.next(a)) {
       const int32_t* bt = a.block_tables + (size_t)(a.seq_begin + w.cur) * a.max_blocks;
-      // The cache row of this lane's block of tile t, one tile ahead.
-      auto tile_row = [&](int t) {
-        const int lb = t * nb + b;
+      // Block ids come 32 at a time, a lane each, with the next 32 on their way:
+      // a load a tile would hold every tile's copies back by its latency.
+      const int blocks = (w.c + a.block_size - 1) / a.block_size;
+      int base = w.t_begin * nb;
+      auto ids_from = [&](int from) { return from + lane < blocks ? bt[from + lane] : -1; };
+      int ids = ids_from(base), ids_next = ids_from(base + 32);
+      for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
+        const int st = g % kStages;
+        if (t * nb - base >= 32) {
+          base += 32;
+          ids = ids_next;
+          ids_next = ids_from(base + 32);
+        }
+        // The cache row of this lane's block; past the context: zeros.
+        const int lb = t * nb + b, phys = __shfl_sync(kFullMask, ids, lb - base);
         int row = a.oob_row;
-        if (t < w.t_end && lb * a.block_size < w.c) {
-          const int phys = bt[lb];
+        if (lb < blocks) {
           if (phys >= 0 && phys < a.num_blocks)
             row = phys * a.block_size;
           else if (lane < nb && rank == 0)
             atomicOr(a.err, PA_ERRBIT_BLOCK_ID);
         }
-        return row;
-      };
-      int row = tile_row(w.t_begin);
-      for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
-        const int st = g % kStages;
         if (g >= kStages)
           ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kKEmpty + st), (g / kStages - 1) & 1));
         if (!ok) break;
@@ -378,7 +384,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d(dst + kAtoms * kAtomBytes + b * a.block_size * 64, &tr,
                         kLatentDim + (int)rank * (kRopeDim / 2), row, bar(kKFull + st));
         }
-        row = tile_row(t + 1);
       }
     }
     if (!ok && lane == 0) {
@@ -389,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpMma) {
     // ---------------- MMA: S of tile i and P.V of tile j, whichever can start.
-    // S has one buffer (the softmax takes it to registers), P two.  One thread
+    // S has two buffers (the softmax takes it to registers), P three.  One thread
     // does all of it: a vote or a warp-wide branch at each step costs more than
     // the step's products.
     if (elect_one()) {
@@ -398,35 +403,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t k_desc = umma_desc_sw128(s_base, 16, 1024);
       const uint64_t r_desc = umma_desc_sw64(s_base + kAtoms * kAtomBytes, 512);
       const uint64_t v_desc = umma_desc_sw128(s_base, kAtomBytes, 1024);
-      const uint64_t p_desc = umma_desc_sw128(s_base + kOffP, 16, 1024);
       constexpr uint64_t kStep = (uint64_t)kStageBytes >> 4;
       int i = 0, j = 0, seg = 0, left = 0;  // left: tiles of i's segment still to come
       unsigned firsts = 0;                  // bit j % 32: tile j starts a segment
       uint64_t t0 = 0;
       unsigned polls = 0;
       while (j < n_tiles) {
-        if (j < i && mbar_test(bar(kPFull + (j & 1)), (j >> 1) & 1)) {
+        if (j < i && mbar_test(bar(kPFull + j % 3), (j / 3) & 1)) {
           // P.V first: it frees a stage and the next P's place.
           const int st = j % kStages;
           const bool first = firsts >> (j % 32) & 1;
           tc_fence_after();
           const uint64_t vd = v_desc + st * kStep;
-          if (j & 1) {
+          const uint32_t pa_ = tmem + col_p(j % 3);
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              umma_f16(tmem, p_desc + (uint64_t)((k * 32) >> 4), vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV,
-                       !first || k > 0);
-          } else {
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              umma_f16_tmem_a(tmem, tmem + kColP + 8 * k, vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV,
-                              !first || k > 0);
-          }
+          for (int k = 0; k < kTile / 16; ++k)
+            umma_f16_tmem_a(tmem, pa_ + 8 * k, vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV, !first || k > 0);
           umma_commit(bar(kKEmpty + st));
-          umma_commit(bar(kOFull + (j & 1)));
+          umma_commit(bar(kOFull + j % 3));
           ++j;
           polls = 0;
-        } else if (i < n_tiles && (i == 0 || mbar_test(bar(kSFree), (i - 1) & 1)) &&
+        } else if (i < n_tiles && (i < 2 || mbar_test(bar(kSFree + (i - 2) % 3), ((i - 2) / 3) & 1)) &&
                    mbar_test(bar(kKFull + i % kStages), (i / kStages) & 1) &&
                    (left > 0 || mbar_test(bar(kQFull), seg & 1))) {
           const int st = i % kStages;
@@ -440,14 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           firsts = (firsts & ~(1u << (i % 32))) | (unsigned)first << (i % 32);
           tc_fence_after();
           const uint64_t kd = k_desc + st * kStep, rd = r_desc + st * kStep;
+          const uint32_t ds = tmem + col_s(i);
 #pragma unroll
           for (int k = 0; k < 16; ++k)
-            umma_f16_tmem_a(tmem + kColS, tmem + kColQ + 8 * k,
+            umma_f16_tmem_a(ds, tmem + kColQ + 8 * k,
                             kd + (uint64_t)(((k / 4) * kAtomBytes + (k % 4) * 32) >> 4), kIdQK, k > 0);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            umma_f16_tmem_a(tmem + kColS, tmem + kColQ + 128 + 8 * k, rd + (uint64_t)((k * 32) >> 4), kIdQK, true);
-          umma_commit(bar(kSFull + (i & 1)));
+            umma_f16_tmem_a(ds, tmem + kColQ + 128 + 8 * k, rd + (uint64_t)((k * 32) >> 4), kIdQK, true);
+          umma_commit(bar(kSFull + i % 3));
           ++i;
           polls = 0;
         } else if ((++polls & 1023) == 0) {
@@ -468,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ---------------- softmax: one head row a thread; warpgroup x takes the
-    // tiles g = x mod 2
+    // tiles g = x mod 3
     const int x = warp >> 2, row = tid & 127;
     const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
     const int h = h0 + row;
@@ -490,28 +488,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0, seg = 0;
     bool ok = true;
     while (ok && w.next(a)) {
-      // The queries to tensor memory, half of them by each group (the last
+      // The queries to tensor memory, some by each group (the last
       // segment's Q K^T products are done: their S has been taken).  Rows past
       // the heads are zero.
       if (live) {
         const __half* q = static_cast<const __half*>(a.query) +
                           ((size_t)(a.seq_begin + w.cur) * a.num_heads + (h < a.num_heads ? h : 0)) * kLatentRow;
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int cb = x == 0 ? k : 3 + k;  // group 0: columns 0-95; group 1: 96-127 and the rotary 16
-          if (cb > 4) break;
-          const uint4* src = reinterpret_cast<const uint4*>(q + (cb < 4 ? rank * kHalf + cb * 64
-                                                                        : kLatentDim + rank * (kRopeDim / 2)));
-          uint32_t r[32];
+        // Columns 32 cb to 32 cb + 31: groups 0 and 1 two of the four each, group
+        // 2 the rotary 16.
+        auto load = [&](const __half* from, uint32_t (&r)[32], int vecs) {
+          const uint4* src = reinterpret_cast<const uint4*>(from);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const uint4 v = (cb < 4 || c < 4) && h < a.num_heads ? src[c] : make_uint4(0, 0, 0, 0);
+            const uint4 v = c < vecs && h < a.num_heads ? src[c] : make_uint4(0, 0, 0, 0);
             r[4 * c] = v.x ^ flip;
             r[4 * c + 1] = v.y ^ flip;
             r[4 * c + 2] = v.z ^ flip;
             r[4 * c + 3] = v.w ^ flip;
           }
-          tmem_st32(tmem + t_lane + kColQ + 32 * cb, r);
+        };
+        uint32_t r[32];
+        if (x < 2) {
+#pragma unroll 1
+          for (int cb = 2 * x; cb < 2 * x + 2; ++cb) {
+            load(q + rank * kHalf + cb * 64, r, 8);
+            tmem_st32(tmem + t_lane + kColQ + 32 * cb, r);
+          }
+        } else {
+          load(q + kLatentDim + rank * (kRopeDim / 2), r, 4);
+          tmem_st16(tmem + t_lane + kColQ + 128, *reinterpret_cast<const uint32_t(*)[16]>(&r[0]));
         }
         tmem_wait_st();
         tc_fence_before();
@@ -520,26 +525,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int g_end = g + w.t_end - w.t_begin;
       float m = -INFINITY, l = 0.f;  // this group's reference and sum
       for (int t = w.t_begin; g < g_end; ++t, ++g) {
-        if ((g & 1) != x) continue;
-        const uint32_t par = (g >> 1) & 1;
+        if (g % 3 != x) continue;
+        const uint32_t par = (g / 3) & 1;
+        const int px = (g + 2) % 3;  // the group of the tile before, and that tile's phase
+        const uint32_t ppar = ((g - 1) / 3) & 1;
         const bool first = t == w.t_begin;
         ok = all(mbar_wait_bounded(bar(kSFull + x), par));
         if (!ok) break;
         uint32_t sr[kTile];
         if (live) {
           tc_fence_after();
-          tmem_ld32(tmem + t_lane + kColS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-          tmem_ld32(tmem + t_lane + kColS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+          tmem_ld32(tmem + t_lane + col_s(g), sr);
           tmem_wait_ld();
           tc_fence_before();
         }
-        mbar_arrive(bar(kSFree));
+        mbar_arrive(bar(kSFree + x));
         uint32_t pk[kTile / 2];
         float alpha = 1.f;
         bool rescale = false;
         if (live) {
           // This CTA's half of the logits to the other one; the other's half.
-          ok = g < 2 || all(mbar_wait_cluster(bar(kXFree + x), par ^ 1));
+          ok = g < 3 || all(mbar_wait_cluster(bar(kXFree + x), par ^ 1));
           if (!ok) break;
 #pragma unroll
           for (int c = 0; c < kTile / 4; ++c)
@@ -570,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // The reference after the tile before.
           float before = -INFINITY;
           if (!first) {
-            ok = all(mbar_wait_bounded(bar(kRef + (x ^ 1)), ((g - 1) >> 1) & 1));
+            ok = all(mbar_wait_bounded(bar(kRef + px), ppar));
             if (!ok) break;
             before = *ref_s;
           }
@@ -580,10 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           alpha = before == -INFINITY || ref == before ? 1.f : exp2_approx(before - ref);
           rescale = __any_sync(kFullMask, alpha != 1.f);
           // The vote needed every lane's values, so the buffer's loads have
-          // returned: it is armed for tile g + 2 and given back.  (A release at
+          // returned: it is armed for tile g + 3 and given back.  (A release at
           // cluster scope would wait for the sends in flight as well: 0.9 us a
           // tile.)
-          if (row == 0 && g + 2 < n_tiles) mbar_arrive_expect_tx(bar(kXFull + x), x_bytes);
+          if (row == 0 && g + 3 < n_tiles) mbar_arrive_expect_tx(bar(kXFull + x), x_bytes);
           if (lane == 0) mbar_arrive_remote(x_free_peer);
           const uint64_t neg2 = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
           float sq[4] = {0.f, 0.f, 0.f, 0.f};
@@ -597,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = ref;
         } else {
           if (!first) {
-            ok = all(mbar_wait_bounded(bar(kRef + (x ^ 1)), ((g - 1) >> 1) & 1));
+            ok = all(mbar_wait_bounded(bar(kRef + px), ppar));
             if (!ok) break;
           }
           mbar_arrive(bar(kRef + x));
@@ -618,12 +624,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // This group's P is free once P.V of its tile before is done; O may be
         // rescaled once that of the other group's is, too.
-        ok = g < 2 || all(mbar_wait_bounded(bar(kOFull + x), par ^ 1));
+        ok = g < 3 || all(mbar_wait_bounded(bar(kOFull + x), par ^ 1));
         if (!ok) break;
         if (live) {
           tc_fence_after();
           if (!first && rescale) {
-            ok = all(mbar_wait_bounded(bar(kOFull + (x ^ 1)), ((g - 1) >> 1) & 1));
+            ok = all(mbar_wait_bounded(bar(kOFull + px), ppar));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1  // seldom taken: unrolled, it costs the loop its registers
@@ -636,17 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st32(tmem + t_lane + cb * 32, r);
             }
           }
-          if (x == 0) {
-            tmem_st32(tmem + t_lane + kColP, pk);
-          } else {
-            unsigned char* p_row = sm + kOffP + row * 128;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<uint4*>(p_row + ((c ^ (row & 7)) << 4)) =
-                  make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-            fence_proxy_async_smem();
-          }
-          tmem_wait_st();  // P, or the rescaled output
+          tmem_st16(tmem + t_lane + col_p(x), pk);
+          tmem_wait_st();
           tc_fence_before();
         }
         mbar_arrive(bar(kPFull + x));
@@ -659,27 +656,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = all(mbar_wait_bounded(bar(kSegA), seg & 1));
       if (!ok) break;
       const int last = g - 1;
-      ok = all(mbar_wait_bounded(bar(kOFull + (last & 1)), (last >> 1) & 1));
+      ok = all(mbar_wait_bounded(bar(kOFull + last % 3), (last / 3) & 1));
       if (!ok) break;
-      // The segment's output, half of it by each group: to `out` when it is the
+      // The segment's output, a third of it by each group: to `out` when it is the
       // whole sequence, else a partial.
       if (live) {
         tc_fence_after();
-        const float2 me = ml_s[(last & 1) * kRows], other = ml_s[((last & 1) ^ 1) * kRows];
-        m = me.x;
-        l = me.y + (other.x == -INFINITY ? 0.f : other.y * exp2_approx(other.x - m));
+        m = ml_s[(last % 3) * kRows].x;
+        l = 0.f;
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+          const float2 v = ml_s[u * kRows];
+          l += v.x == -INFINITY ? 0.f : v.y * exp2_approx(v.x - m);
+        }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const bool whole = w.t_begin == 0 && w.t_end == w.n;
         const size_t sh = (size_t)(a.seq_begin + w.cur) * a.num_heads + h;
         const size_t ph = (size_t)(w.cur + worker) * a.num_heads + h;
         if (!whole && rank == 0 && x == 0 && h < a.num_heads) a.ws_ml[ph] = make_float2(m, l);
-        const int d0 = rank * kHalf + x * (kHalf / 2);
-        __half* orow = static_cast<__half*>(a.out) + sh * kLatentDim + d0;
-        float* prow = a.ws_o + ph * kLatentDim + d0;
+        __half* orow = static_cast<__half*>(a.out) + sh * kLatentDim + rank * kHalf;
+        float* prow = a.ws_o + ph * kLatentDim + rank * kHalf;
 #pragma unroll 1
-        for (int cb = 0; cb < kHalf / 64; ++cb) {
+        for (int cb = x; cb < kHalf / 32; cb += kGroups) {
           uint32_t r[32];
-          tmem_ld32(tmem + t_lane + x * (kHalf / 2) + cb * 32, r);
+          tmem_ld32(tmem + t_lane + cb * 32, r);
           tmem_wait_ld();
           if (h < a.num_heads) {
             if (whole) {

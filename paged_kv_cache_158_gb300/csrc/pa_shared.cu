@@ -391,20 +391,27 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
     auto uni = [&](bool v) { return __all_sync(kFullMask, v); };
     while (ok && w.next(a)) {
       const int32_t* bt = a.block_tables + (size_t)w.leader * a.max_blocks;
-      auto tile_row = [&](int t) {  // cache row of this lane's block, one tile ahead
-        const int lb = t * bpt + lane;
+      // Block ids come 32 at a time, a lane each, with the next 32 on their way:
+      // a load a tile would hold every tile's copies back by its latency.
+      const int blocks = w.prefix / a.block_size;
+      int base = w.t_begin * bpt;
+      auto ids_from = [&](int from) { return from + lane < blocks ? bt[from + lane] : -1; };
+      int ids = ids_from(base), ids_next = ids_from(base + 32);
+      for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
+        if (t * bpt - base >= 32) {
+          base += 32;
+          ids = ids_next;
+          ids_next = ids_from(base + 32);
+        }
+        // The cache row of this lane's block; past the prefix: zeros.
+        const int lb = t * bpt + lane, phys = __shfl_sync(kFullMask, ids, (lb - base) & 31);
         int row = a.oob_row;
-        if (lane < bpt && t < w.t_end && lb * a.block_size < w.prefix) {
-          const int phys = bt[lb];
+        if (lane < bpt && lb < blocks) {
           if (phys >= 0 && phys < a.num_blocks)
             row = (phys * a.num_heads + w.h) * a.block_size;
           else
             atomicOr(a.err, PA_ERRBIT_BLOCK_ID);
         }
-        return row;
-      };
-      int row = tile_row(w.t_begin);
-      for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           uint32_t dst, full;
@@ -434,7 +441,6 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
           ++(kv ? vi : ki);
         }
         if (!ok) break;
-        row = tile_row(t + 1);
       }
     }
     if (!ok && lane == 0) {
