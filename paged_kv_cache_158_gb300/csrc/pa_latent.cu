@@ -103,8 +103,8 @@ constexpr int kRopeBytes = kTile * kRopeDim;  // its half of the rotary values
 constexpr int kStageBytes = kAtoms * kAtomBytes + kRopeBytes;
 constexpr int kStages = 9;
 constexpr int kGroups = 3;             // softmax warpgroups
-constexpr int kThreads = 128 * kGroups + 64;
-constexpr int kWarpTma = 4 * kGroups, kWarpMma = kWarpTma + 1;
+constexpr int kThreads = 128 * kGroups + 96;
+constexpr int kWarpTma = 4 * kGroups, kWarpQk = kWarpTma + 1, kWarpPv = kWarpTma + 2;
 constexpr int kSeqsPerLaunch = 1024;
 
 constexpr int kXBytes = kRows * kTile * 4;                 // one half of S from the other CTA
@@ -127,7 +127,7 @@ constexpr float kRescale = 8.f;        // base-2 logits above the reference that
 enum {
   kKFull = 0 /* 9 */, kKEmpty = 9 /* 9 */, kQFull = 18, kSFull = 19 /* 3 */, kSFree = 22 /* 3 */, kPFull = 25 /* 3 */,
   kOFull = 28 /* 3 */, kXFull = 31 /* 3 */, kXFree = 34 /* 3 */, kRef = 37 /* 3 */, kSegA = 40, kSegB = 41, kDone = 42,
-  kDrain = 43, kNumBars = 44
+  kDrain = 43 /* 2 */, kNumBars = 45
 };
 
 struct LatentParams {
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int worker = cluster / a.head_tiles, ht = cluster % a.head_tiles;
   const int h0 = ht * kRows;
   const int live_warps = min(4, (a.num_heads - h0 + 31) / 32);  // softmax warps with heads
-  if (tid == kWarpMma * 32) {
+  if (tid == kWarpQk * 32) {
     for (int i = 0; i < kNumBars; ++i)
       mbar_init(bar(i), (i >= kSFree && i < kOFull) || (i >= kRef && i < kSegA) ? 128
                         : i == kQFull || i == kSegA || i == kSegB               ? 128 * kGroups
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpTma) {
     // ---------------- TMA: the tiles of the range
     const int nb = kTile / a.block_size;
-    const int b = lane % nb;
+    const int b = lane & (nb - 1);
     int g = 0;
     bool ok = true;
     while (ok && w.next(a)) {
@@ -369,21 +369,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           else if (lane < nb && rank == 0)
             atomicOr(a.err, PA_ERRBIT_BLOCK_ID);
         }
-        if (g >= kStages)
-          ok = __all_sync(kFullMask, mbar_wait_bounded(bar(kKEmpty + st), (g / kStages - 1) & 1));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + st), kStageBytes);
-        __syncwarp();
-        const uint32_t dst = s_base + st * kStageBytes;
-        for (int i = lane; i < (kAtoms + 1) * nb; i += 32) {
-          const int at = i / nb;
-          if (at < kAtoms)
-            tma_load_2d(dst + at * kAtomBytes + b * a.block_size * 128, &tc, (int)rank * kHalf + at * 64, row,
-                        bar(kKFull + st));
-          else
-            tma_load_2d(dst + kAtoms * kAtomBytes + b * a.block_size * 64, &tr,
-                        kLatentDim + (int)rank * (kRopeDim / 2), row, bar(kKFull + st));
+        int rows[4];  // of the tile's blocks (at most 32 / 8)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) rows[u] = __shfl_sync(kFullMask, row, u);
+        // One thread waits and issues: the copies' operands stay uniform.
+        bool mine = true;
+        if (elect_one()) {
+          mine = g < kStages || mbar_wait_bounded(bar(kKEmpty + st), (g / kStages - 1) & 1);
+          if (mine) {
+            mbar_arrive_expect_tx(bar(kKFull + st), kStageBytes);
+            const uint32_t dst = s_base + st * kStageBytes;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if (u >= nb) break;
+#pragma unroll
+              for (int at = 0; at < kAtoms; ++at)
+                tma_load_2d(dst + at * kAtomBytes + u * a.block_size * 128, &tc, (int)rank * kHalf + at * 64,
+                            rows[u], bar(kKFull + st));
+              tma_load_2d(dst + kAtoms * kAtomBytes + u * a.block_size * 64, &tr,
+                          kLatentDim + (int)rank * (kRopeDim / 2), rows[u], bar(kKFull + st));
+            }
+          }
         }
+        ok = __all_sync(kFullMask, mine);
+        if (!ok) break;
       }
     }
     if (!ok && lane == 0) {
@@ -392,75 +401,93 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = max(0, g - kStages); u < g; ++u)
         mbar_wait_bounded(bar(kKFull + u % kStages), (u / kStages) & 1);
     }
-  } else if (warp == kWarpMma) {
-    // ---------------- MMA: S of tile i and P.V of tile j, whichever can start.
-    // S has two buffers (the softmax takes it to registers), P three.  One thread
-    // does all of it: a vote or a warp-wide branch at each step costs more than
-    // the step's products.
+  } else if (warp == kWarpQk) {
+    // ---------------- S = Q K^T, one thread.  (One thread for these products
+    // and P.V spends 0.2 us a product on finding out which can start: 0.35 us
+    // each, and no lighter load, exchange or softmax made a tile faster.)
     if (elect_one()) {
-      constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
-      constexpr uint32_t kIdPV = umma_idesc_f16(kRows, kHalf, false, true);
+      constexpr uint32_t kId = umma_idesc_f16(kRows, kTile, false, false);
       const uint64_t k_desc = umma_desc_sw128(s_base, 16, 1024);
       const uint64_t r_desc = umma_desc_sw64(s_base + kAtoms * kAtomBytes, 512);
+      constexpr uint64_t kStep = (uint64_t)kStageBytes >> 4;
+      int seg = 0, left = 0, st = 0, g3 = 0;  // left: tiles of the segment still to come
+      uint32_t ph = 0;                        // phase of the stage
+      bool ok = true;
+      for (int i = 0; i < n_tiles; ++i) {
+        if (left == 0) {
+          w.next(a);
+          left = w.t_end - w.t_begin;
+          ok = mbar_wait_bounded(bar(kQFull), seg & 1);
+          ++seg;
+        }
+        --left;
+        // S(i) takes the place of S(i - 2), once that is in registers; the tile.
+        if (i >= 2) ok = ok && mbar_wait_bounded(bar(kSFree + (i - 2) % 3), ((i - 2) / 3) & 1);
+        ok = ok && mbar_wait_bounded(bar(kKFull + st), ph);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t kd = k_desc + st * kStep, rd = r_desc + st * kStep;
+        const uint32_t ds = tmem + col_s(i);
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          umma_f16_tmem_a(ds, tmem + kColQ + 8 * k, kd + (uint64_t)(((k / 4) * kAtomBytes + (k % 4) * 32) >> 4), kId,
+                          k > 0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          umma_f16_tmem_a(ds, tmem + kColQ + 128 + 8 * k, rd + (uint64_t)((k * 32) >> 4), kId, true);
+        umma_commit(bar(kSFull + g3));
+        if (++g3 == 3) g3 = 0;
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+      if (!ok) {
+        atomicOr(a.err, PA_ERRBIT_TIMEOUT);
+        *fail = 1;
+        // Every product started ends (bounded) before its memory goes.
+        umma_commit(bar(kDrain));
+        mbar_wait_bounded(bar(kDrain), 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpPv) {
+    // ---------------- O += P V, one thread
+    if (elect_one()) {
+      constexpr uint32_t kId = umma_idesc_f16(kRows, kHalf, false, true);
       const uint64_t v_desc = umma_desc_sw128(s_base, kAtomBytes, 1024);
       constexpr uint64_t kStep = (uint64_t)kStageBytes >> 4;
-      int i = 0, j = 0, seg = 0, left = 0;  // left: tiles of i's segment still to come
-      unsigned firsts = 0;                  // bit j % 32: tile j starts a segment
-      uint64_t t0 = 0;
-      unsigned polls = 0;
-      while (j < n_tiles) {
-        if (j < i && mbar_test(bar(kPFull + j % 3), (j / 3) & 1)) {
-          // P.V first: it frees a stage and the next P's place.
-          const int st = j % kStages;
-          const bool first = firsts >> (j % 32) & 1;
-          tc_fence_after();
-          const uint64_t vd = v_desc + st * kStep;
-          const uint32_t pa_ = tmem + col_p(j % 3);
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            umma_f16_tmem_a(tmem, pa_ + 8 * k, vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV, !first || k > 0);
-          umma_commit(bar(kKEmpty + st));
-          umma_commit(bar(kOFull + j % 3));
-          ++j;
-          polls = 0;
-        } else if (i < n_tiles && (i < 2 || mbar_test(bar(kSFree + (i - 2) % 3), ((i - 2) / 3) & 1)) &&
-                   mbar_test(bar(kKFull + i % kStages), (i / kStages) & 1) &&
-                   (left > 0 || mbar_test(bar(kQFull), seg & 1))) {
-          const int st = i % kStages;
-          const bool first = left == 0;
-          if (first) {
-            w.next(a);
-            left = w.t_end - w.t_begin;
-            ++seg;
-          }
-          --left;
-          firsts = (firsts & ~(1u << (i % 32))) | (unsigned)first << (i % 32);
-          tc_fence_after();
-          const uint64_t kd = k_desc + st * kStep, rd = r_desc + st * kStep;
-          const uint32_t ds = tmem + col_s(i);
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            umma_f16_tmem_a(ds, tmem + kColQ + 8 * k,
-                            kd + (uint64_t)(((k / 4) * kAtomBytes + (k % 4) * 32) >> 4), kIdQK, k > 0);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            umma_f16_tmem_a(ds, tmem + kColQ + 128 + 8 * k, rd + (uint64_t)((k * 32) >> 4), kIdQK, true);
-          umma_commit(bar(kSFull + i % 3));
-          ++i;
-          polls = 0;
-        } else if ((++polls & 1023) == 0) {
-          // The timer is read now and then only: it takes as long as a product.
-          const uint64_t now = global_timer_ns();
-          if (polls == 1024) t0 = now;
-          if (now - t0 > kWaitLimitNs || *fail) {
-            atomicOr(a.err, PA_ERRBIT_TIMEOUT);
-            *fail = 1;
-            // Every product started ends (bounded) before its memory goes.
-            umma_commit(bar(kDrain));
-            mbar_wait_bounded(bar(kDrain), 0);
-            break;
-          }
+      int left = 0, st = 0, g3 = 0;
+      uint32_t ph3 = 0;
+      bool ok = true;
+      for (int j = 0; j < n_tiles; ++j) {
+        const bool first = left == 0;  // a segment's first product overwrites
+        if (first) {
+          w.next(a);
+          left = w.t_end - w.t_begin;
         }
+        --left;
+        ok = mbar_wait_bounded(bar(kPFull + g3), ph3);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = v_desc + st * kStep;
+        const uint32_t pt = tmem + col_p(g3);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          umma_f16_tmem_a(tmem, pt + 8 * k, vd + (uint64_t)((k * 16 * 128) >> 4), kId, !first || k > 0);
+        umma_commit(bar(kKEmpty + st));
+        umma_commit(bar(kOFull + g3));
+        if (++g3 == 3) {
+          g3 = 0;
+          ph3 ^= 1;
+        }
+        if (++st == kStages) st = 0;
+      }
+      if (!ok) {
+        atomicOr(a.err, PA_ERRBIT_TIMEOUT);
+        *fail = 1;
+        umma_commit(bar(kDrain + 1));
+        mbar_wait_bounded(bar(kDrain + 1), 0);
       }
     }
     __syncwarp();
