@@ -26,11 +26,11 @@
 //    4 H s0 + h * rows + 128 w (s0: the unit's first sequence; w: the worker;
 //    rows: the unit's, copies counted), distinct because along the walk either
 //    the unit or w grows.
-//  * Warps: four softmax warps (one query row a thread), TMA, MMA, and for
+//  * Warps: four softmax warps (one query row a thread), TMA, Q K^T, P V, and for
 //    E4M3 caches eight that widen the codes to fp16 in shared memory (exact).
 //    The queries are the A operand from tensor memory, S has four buffers
-//    there, P (fp16, rounded once) lies over the first half of its S, and the
-//    products of S and P.V are issued in the order in which they become ready.
+//    there, P (fp16, rounded once) lies over the first half of its S, and one
+//    thread issues the products Q K^T, another those of P.V.
 //  * Copies: a tile's softmax takes a warp 0.7 us whatever the rows, and the
 //    products 128 rows whatever the members, so a unit of up to 32 (64) members
 //    has its queries in the lanes four (two) times and each copy's warps take
@@ -269,7 +269,7 @@ struct Traits {
   static constexpr int USED = OFF_BAR + 512 + 1024;
   // At least 115 KB, so that two do not share an SM.
   static constexpr int SMEM = USED > 115 * 1024 ? USED : 115 * 1024;
-  static constexpr int THREADS = F8 ? 448 : 192;
+  static constexpr int THREADS = F8 ? 480 : 224;
   static constexpr uint32_t COL_Q = kBuffers * kTile;  // S: kTile columns each
   static constexpr uint32_t COL_O = COL_Q + 2 * 64;    // Q: D / 2 columns, this segment's and the next's; O: D
   static_assert(COL_O + D <= 512, "tensor memory");
@@ -278,10 +278,11 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;  // base-2 logits above the reference that move it
 
 // Barriers.  S, P and O have one for each buffer of S (tile g mod 4): their
-// phases are not all waited for, and S(g) only says that P.V(g - 4) is done, so
-// a single barrier's parity could be taken for an earlier phase.
+// phases are not all waited for by one thread, and S(g) only says that
+// P.V(g - 4) is done, so a single barrier's parity could be taken for an earlier
+// phase.
 enum {
-  kQFull = 47 /* 2 */, kDone = 1, kDrain = 2, kKFull = 3, kKEmpty = 7, kVFull = 11, kVEmpty = 15, kSFull = 19, kPFull = 23,
+  kDrain2 = 0, kQFull = 47 /* 2 */, kDone = 1, kDrain = 2, kKFull = 3, kKEmpty = 7, kVFull = 11, kVEmpty = 15, kSFull = 19, kPFull = 23,
   kOFull = 27, kCFull = 31 /* K 4, V 4 */, kCEmpty = 39 /* K 4, V 4 */, kNumBars = 49
 };
 
@@ -290,20 +291,6 @@ __device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 2 : 1; 
 // First partial row of a segment.
 __device__ __forceinline__ size_t partial_row(int H, int s0, int h, int rows, int copies, int worker) {
   return (size_t)H * s0 * 4 + (size_t)h * rows * copies + (size_t)worker * kRows;
-}
-
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n"
-      "  .reg .pred p;\n"
-      "  mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      "  selp.u32 %0, 1, 0, p;\n"
-      "}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 // Widens one tile of codes (row-major) into the swizzled fp16 operand layout:
@@ -453,69 +440,86 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
         mbar_wait_bounded(bar((F8 ? kCFull + 4 : kVFull) + u % N), (u / N) & 1);
     }
   } else if (warp == 5) {
-    // ---------------- MMA: S of tile i or P.V of tile j, whichever can start.
-    // One thread does all of it: a vote or a warp-wide branch at each step costs
-    // more than the step's products.
+    // ---------------- S = Q K^T, one thread
     if (elect_one()) {
-      constexpr uint32_t kIdQK = umma_idesc_f16(kRows, kTile, false, false);
-      constexpr uint32_t kIdPV = umma_idesc_f16(kRows, D, false, true);
+      constexpr uint32_t kId = umma_idesc_f16(kRows, kTile, false, false);
       const uint64_t k_desc = umma_desc_sw128(s_base, 16, 1024);
+      constexpr uint64_t kStep = (uint64_t)T::TB >> 4;
+      int seg = -1, left = 0, st = 0;  // left: tiles of the segment still to come
+      uint32_t ph = 0;                 // phase of the stage
+      bool ok = true;
+      for (int i = 0; i < n_tiles; ++i) {
+        if (left == 0) {
+          w.next(a);
+          left = w.t_end - w.t_begin;
+          ++seg;
+          ok = mbar_wait_bounded(bar(kQFull + (seg & 1)), (seg >> 1) & 1);
+        }
+        --left;
+        // S(i) and P(i) take the place of S(i - 4), P(i - 4); the tile.
+        if (i >= kBuffers) ok = ok && mbar_wait_bounded(bar(kOFull + (i & 3)), ((i >> 2) - 1) & 1);
+        ok = ok && mbar_wait_bounded(bar(kKFull + st), ph);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t kd = k_desc + st * kStep;
+        const uint32_t qa = tmem + T::COL_Q + 64 * (seg & 1);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = (uint64_t)(((k / 4) * T::ATOM + (k % 4) * 32) >> 4);
+          umma_f16_tmem_a(tmem + kTile * (i & 3), qa + 8 * k, kd + off, kId, k > 0);
+        }
+        umma_commit(bar(kSFull + (i & 3)));
+        umma_commit(bar(kKEmpty + st));
+        if (++st == NST) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+      if (!ok) {
+        atomicOr(a.err, PA_ERRBIT_TIMEOUT);
+        *fail = 1;
+        // Every product started ends (bounded) before its memory goes.
+        umma_commit(bar(kDrain));
+        mbar_wait_bounded(bar(kDrain), 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ---------------- O += P V, one thread
+    if (elect_one()) {
+      constexpr uint32_t kId = umma_idesc_f16(kRows, D, false, true);
       const uint64_t v_desc = umma_desc_sw128(s_base + T::OFF_V, T::ATOM, 1024);
       constexpr uint64_t kStep = (uint64_t)T::TB >> 4;
-      int i = 0, j = 0, seg = -1, left = 0;  // left: tiles of i's segment still to come
-      unsigned firsts = 0;                   // bit j % 32: tile j starts a segment
-      uint64_t t0 = 0;
-      unsigned polls = 0;
-      while (j < n_tiles) {
-        if (j < i && mbar_test(bar(kPFull + (j & 3)), (j >> 2) & 1) &&
-            mbar_test(bar(kVFull + j % NST), (j / NST) & 1)) {
-          // P.V first: it frees a stage and a buffer of S.
-          tc_fence_after();
-          const bool first = firsts >> (j % 32) & 1;
-          const uint64_t vd = v_desc + (j % NST) * kStep;
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            umma_f16_tmem_a(tmem + T::COL_O, tmem + kTile * (j & 3) + 8 * k,
-                            vd + (uint64_t)((k * 16 * 128) >> 4), kIdPV, !first || k > 0);
-          umma_commit(bar(kVEmpty + j % NST));
-          umma_commit(bar(kOFull + (j & 3)));
-          ++j;
-          polls = 0;
-        } else if (i < n_tiles && i < j + kBuffers && mbar_test(bar(kKFull + i % NST), (i / NST) & 1) &&
-                   (left > 0 || mbar_test(bar(kQFull + ((seg + 1) & 1)), ((seg + 1) >> 1) & 1))) {
-          tc_fence_after();
-          const bool first = left == 0;
-          if (first) {
-            w.next(a);
-            left = w.t_end - w.t_begin;
-            ++seg;
-          }
-          firsts = (firsts & ~(1u << (i % 32))) | (unsigned)first << (i % 32);
-          --left;
-          const uint64_t kd = k_desc + (i % NST) * kStep;
-          const uint32_t qa = tmem + T::COL_Q + 64 * (seg & 1);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = (uint64_t)(((k / 4) * T::ATOM + (k % 4) * 32) >> 4);
-            umma_f16_tmem_a(tmem + kTile * (i & 3), qa + 8 * k, kd + off, kIdQK, k > 0);
-          }
-          umma_commit(bar(kSFull + (i & 3)));
-          umma_commit(bar(kKEmpty + i % NST));
-          ++i;
-          polls = 0;
-        } else if ((++polls & 1023) == 0) {
-          // The timer is read now and then only: it takes as long as a product.
-          const uint64_t now = global_timer_ns();
-          if (polls == 1024) t0 = now;
-          if (now - t0 > kWaitLimitNs || *fail) {
-            atomicOr(a.err, PA_ERRBIT_TIMEOUT);
-            *fail = 1;
-            // Every product started ends (bounded) before its memory goes.
-            umma_commit(bar(kDrain));
-            mbar_wait_bounded(bar(kDrain), 0);
-            break;
-          }
+      int left = 0, st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int j = 0; j < n_tiles; ++j) {
+        const bool first = left == 0;  // a segment's first product overwrites
+        if (first) {
+          w.next(a);
+          left = w.t_end - w.t_begin;
         }
+        --left;
+        ok = mbar_wait_bounded(bar(kPFull + (j & 3)), (j >> 2) & 1) && mbar_wait_bounded(bar(kVFull + st), ph);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = v_desc + st * kStep;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          umma_f16_tmem_a(tmem + T::COL_O, tmem + kTile * (j & 3) + 8 * k, vd + (uint64_t)((k * 16 * 128) >> 4), kId,
+                          !first || k > 0);
+        umma_commit(bar(kVEmpty + st));
+        umma_commit(bar(kOFull + (j & 3)));
+        if (++st == NST) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+      if (!ok) {
+        atomicOr(a.err, PA_ERRBIT_TIMEOUT);
+        *fail = 1;
+        umma_commit(bar(kDrain2));
+        mbar_wait_bounded(bar(kDrain2), 0);
       }
     }
     __syncwarp();
@@ -665,7 +669,7 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
     // ---------------- E4M3 caches: four warps widen the staged codes of K, four
     // those of V (apart, so that a V stage still in use does not hold back the
     // next K; with two and two a tile took them 0.6 us, half of it latency)
-    const int kv = (warp - 6) >> 2, i = (tid - 192) & 127;
+    const int kv = (warp - 7) >> 2, i = (tid - 224) & 127;
     int g = 0;
     bool ok = true;
     while (ok && w.next(a)) {
