@@ -138,6 +138,21 @@ __device__ __forceinline__ int last_at_most(const int* starts, int lo, int hi, i
   return lo;
 }
 
+// The same by a whole warp, 32 probes at a time: the probes' loads are one
+// latency, and a few thousand sequences are three of them, not a dozen.
+__device__ __forceinline__ int last_at_most_warp(const int* starts, int lo, int hi, int t) {
+  const int lane = threadIdx.x & 31;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;  // probes lo + step, lo + 2 step, ...
+    const int at = lo + step * (lane + 1);
+    const unsigned le = __ballot_sync(kFullMask, at <= hi && starts[at] <= t);
+    const int n = __popc(le);              // starts do not decrease: the first n
+    lo += step * n;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
 // Inclusive sums of (x, y) over the block; the totals in *tx, *ty.  `sums`:
 // 64 values of shared memory.
 __device__ __forceinline__ void block_scan2(long long& x, long long& y, long long* sums,
@@ -296,7 +311,10 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TablesP
     const int t0 = (int)blockIdx.x * kFillTokens;
     const int t1 = min(t0 + kFillTokens, a.num_slots) - 1;
     // The sequences of the CTA's first and last token bound every search.
-    if (tid < 2) range[tid] = last_at_most(a.query_start, 0, S - 1, tid == 0 ? t0 : t1);
+    if (tid < 64) {
+      const int s = last_at_most_warp(a.query_start, 0, S - 1, tid < 32 ? t0 : t1);
+      if ((tid & 31) == 0) range[tid >> 5] = s;
+    }
     __syncthreads();
     const int lo = range[0], hi = range[1];
     for (int t = t0 + tid; t <= t1; t += kFillThreads) {
