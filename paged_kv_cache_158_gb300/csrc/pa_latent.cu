@@ -500,13 +500,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t scale2 = f32x2_splat(scale);
     int g = 0, seg = 0;
     bool ok = true;
-    while (ok && w.next(a)) {
-      // The queries to tensor memory, some by each group (the last
-      // segment's Q K^T products are done: their S has been taken).  Rows past
-      // the heads are zero.
+    // The queries of a segment to tensor memory, some by each group.  Rows past
+    // the heads are zero.
+    auto load_queries = [&](const Walk& n) {
       if (live) {
         const __half* q = static_cast<const __half*>(a.query) +
-                          ((size_t)(a.seq_begin + w.cur) * a.num_heads + (h < a.num_heads ? h : 0)) * kLatentRow;
+                          ((size_t)(a.seq_begin + n.cur) * a.num_heads + (h < a.num_heads ? h : 0)) * kLatentRow;
         // Columns 32 cb to 32 cb + 31: groups 0 and 1 two of the four each, group
         // 2 the rotary 16.
         auto load = [&](const __half* from, uint32_t (&r)[32], int vecs) {
@@ -535,6 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
       }
       mbar_arrive(bar(kQFull));
+    };
+    Walk ahead = w;
+    bool more = ahead.next(a);
+    if (more) load_queries(ahead);
+    while (ok && more) {
+      w = ahead;
+      more = ahead.next(a);
       const int g_end = g + w.t_end - w.t_begin;
       float m = -INFINITY, l = 0.f;  // this group's reference and sum
       for (int t = w.t_begin; g < g_end; ++t, ++g) {
@@ -668,6 +674,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(bar(kSegA));
       ok = all(mbar_wait_bounded(bar(kSegA), seg & 1));
       if (!ok) break;
+      // Every S of the segment has been taken, so its products with the queries
+      // are done: the next segment's first ones run beside this one's epilogue.
+      if (more) load_queries(ahead);
       const int last = g - 1;
       ok = all(mbar_wait_bounded(bar(kOFull + last % 3), (last / 3) & 1));
       if (!ok) break;
