@@ -340,7 +340,7 @@ pa_status decode_shared_impl(bool fp8, void* out, const void* query, const void*
   // 32-bit item, tile and row numbers.
   const long long units = ((long long)num_seqs / 128 + num_groups) * num_heads;
   if ((long long)num_seqs * num_heads * w.max_parts >= (1LL << 31) ||
-      units * (max_prefix_len / 128 + 1) >= (1LL << 31) ||
+      units * (max_prefix_len / pa::kSharedTile + 1) >= (1LL << 31) ||
       !pa::prefill_rows_fit(num_blocks, num_heads, block_size))
     return PA_ERR_UNSUPPORTED;
   DeviceState ds;
@@ -844,14 +844,17 @@ pa_status pa_build_tables(int32_t* block_tables, int max_blocks_per_seq, int32_t
       workspace_bytes < pa_build_tables_workspace_size(num_seqs))
     return PA_ERR_INVALID_ARG;
   // The new lengths, the query starts and the tables are written while others
-  // of these are still read.
-  const void* written[] = {context_lens, query_start, num_free_out, block_tables};
+  // of these are still read, and no array is written twice.
+  const void* written[] = {context_lens, query_start, num_free_out, block_tables, slot_mapping};
   const void* read[] = {new_lens, group_start, prefix_blocks, free_list, cached_lens, num_free};
   for (const void* w : written)
     for (const void* r : read)
       if (w && w == r && !(w == context_lens && r == cached_lens) &&
           !(w == num_free_out && r == num_free))
         return PA_ERR_INVALID_ARG;
+  for (const void* const& w : written)
+    for (const void* const& v : written)
+      if (w && w == v && &w != &v) return PA_ERR_INVALID_ARG;
   if ((long long)num_seqs * max_blocks_per_seq >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
   DeviceState ds;
   pa_status st = device_state(&ds, false);
@@ -936,6 +939,12 @@ pa_status pa_latent_decode(void* out, const void* query, const void* cache,
     return PA_ERR_INVALID_ARG;
   if (workspace_bytes < pa_latent_decode_workspace_size(num_seqs, num_heads))
     return PA_ERR_INVALID_ARG;
+  // 32-bit tile numbers of a launch.
+  const long long longest =
+      std::min((long long)max_blocks_per_seq * block_size, (long long)max_context_len);
+  if ((long long)std::min(num_seqs, pa::kLatentSeqsPerLaunch) *
+          ((longest + pa::kLatentTile - 1) / pa::kLatentTile) >= (1LL << 31))
+    return PA_ERR_UNSUPPORTED;
   // 32-bit row coordinates of the copies (one past the last row included).
   if ((long long)num_blocks * block_size >= (1LL << 31) - 64 ||
       (long long)num_seqs * num_heads >= (1LL << 31) - 64)

@@ -164,6 +164,14 @@ __device__ __forceinline__ void cp_async_wait_all() {
 
 // ---- arithmetic ----------------------------------------------------------
 
+// |scale| as a factor of masked logits: -inf times it stays -inf, so a scale of
+// 0 (every logit 0) becomes the smallest normal number.
+__device__ __forceinline__ float multiplier(float scale) {
+  constexpr float kSmallest = 1.17549435e-38f;
+  const float s = fabsf(scale);
+  return s < kSmallest ? kSmallest : s;
+}
+
 // 2^x (the SFU's approximate exponential; relative error about 2^-22).
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;

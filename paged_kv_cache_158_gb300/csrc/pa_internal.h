@@ -165,6 +165,8 @@ cudaError_t launch_build_tables(const TablesParams& p, cudaStream_t stream);
 constexpr int kLatentDim = 512;
 constexpr int kRopeDim = 64;
 constexpr int kLatentRow = kLatentDim + kRopeDim;
+constexpr int kLatentTile = 32;            // tokens of a tile of the decode
+constexpr int kLatentSeqsPerLaunch = 1024;
 
 // Strides in 16-byte vectors.
 cudaError_t launch_latent_write(const void* latent, long long latent_stride, const void* rope,
@@ -185,6 +187,8 @@ struct LatentArgs {
 };
 size_t latent_workspace_bytes(int num_seqs, int num_heads, int sms);
 cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream);
+
+constexpr int kSharedTile = 64;  // tokens of a tile of the prefix pass
 
 // Decode of a batch whose groups of sequences share a prefix: arguments as in
 // pa_decode_shared, and the suffix pass's partials.

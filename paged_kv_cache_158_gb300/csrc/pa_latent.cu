@@ -14,7 +14,7 @@
 // with 128 heads 242: HBM and tensor cores together.
 //
 // Design (GB300):
-//  * A cluster of two CTAs takes (128 heads) x (a range of 64-token tiles): the
+//  * A cluster of two CTAs takes (128 heads) x (a range of 32-token tiles): the
 //    batch's tiles, numbered sequence by sequence, are cut into equal ranges,
 //    one for each cluster, so ragged batches and single long contexts alike
 //    load every SM to within a tile.  More than 128 heads: the clusters of one
@@ -28,27 +28,38 @@
 //  * The two CTAs split the row's values, not the tokens: CTA r holds latent
 //    values [256 r, 256 r + 256) and contracts those and half of the rotary
 //    ones, so S = Q K^T is the sum of two halves, exchanged through
-//    distributed shared memory (st.async, 32 KB a tile and direction); each
+//    distributed shared memory (st.async, 16 KB a tile and direction); each
 //    CTA then computes the same weights P and O += P V for its 256 values.
 //    The reason is the tensor memory: 128 rows x 512 fp32 of output would fill
 //    it.  (64 heads a CTA with all 512 values in 256 columns x both halves of
 //    the lanes were built first: M = 64 products take as long as M = 128 ones,
-//    a tile cost 1.3 us for Q K^T and 0.65 us for P V, and 64 sequences of
-//    4096-8192 tokens with 128 heads took 246 us.)
+//    and 64 sequences of 4096-8192 tokens with 128 heads took 246 us.)
 //  * The queries (fp16, 144 columns) are the A operand of Q K^T from tensor
-//    memory, so a product of 64 tokens reads 2 KB of shared memory, not 6, and
-//    the shared memory holds four stages of rows.
-//  * A stage is 64 rows of the CTA's 256 latent values (four 64-value atoms of
+//    memory, so a product reads the tile's shared memory alone.
+//  * A stage is 32 rows of the CTA's 256 latent values (four 64-value atoms of
 //    128-byte swizzle) and its 32 rotary ones (64-byte swizzle), copied by TMA
 //    one box a block and atom; it is the K operand of Q K^T and, its four atoms
-//    read the other way round, the V operand of P V.
-//  * Two softmax warpgroups (one head row a thread) take alternate tiles, so
-//    one's exchange overlaps the other's exponentials.  The row's reference
-//    goes from tile to tile through shared memory; each group keeps the sum of
-//    its own tiles, joined at the segment's end.  References and sums are
-//    fp32, P is rounded once to fp16 (the sum adds the rounded weights).  The
-//    reference moves only when the tile's maximum is more than 2^8 above it,
-//    so the output is seldom rescaled.
+//    read the other way round, the V operand of P V.  Nine stages are in
+//    flight.
+//  * Three softmax warpgroups (one head row a thread) take the tiles in turn:
+//    a tile's chain (product, exchange, softmax, product) takes 2 us, most of
+//    it waiting, so three tiles are on their way at a time.  (Two groups on
+//    64-token tiles: the same 64 sequences 172 us, three on 32-token ones 154;
+//    four, 160: their registers spill.)  The row's reference goes from tile to
+//    tile through shared memory; each group keeps the sum of its own tiles,
+//    joined at the segment's end.  References and sums are fp32, P is rounded
+//    once to fp16 (the sum adds the rounded weights).  The reference moves only
+//    when the tile's maximum is more than 2^8 above it, so the output is
+//    seldom rescaled.
+//  * Copies, Q K^T and P V are issued by a thread each, in three warps of their
+//    own.  A segment's queries are loaded beside the epilogue of the one
+//    before.
+//
+// Measured (inputs out of L2): 4 sequences of 16-300 tokens, 16 heads, 11 us,
+// most of it launches and one tile's chain; two of 60-100 thousand, 64 heads,
+// 60 us (46% of the HBM floor); 64 of 4096-8192, 128 heads, 151 us (47%).  What
+// bounds them is that chain: 0.6-0.8 us a tile in the steady state, where HBM
+// would need 0.36, and about 5 us at each change of sequence within a range.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -95,7 +106,7 @@ __global__ void __launch_bounds__(256)
 // ---- decode -----------------------------------------------------------------
 
 constexpr int kRows = 128;             // head rows of a cluster (MMA M)
-constexpr int kTile = 32;              // tokens of a tile
+constexpr int kTile = kLatentTile;     // tokens of a tile
 constexpr int kHalf = kLatentDim / 2;  // output values of a CTA
 constexpr int kAtoms = 4;              // its 64-value atoms of latent values
 constexpr int kAtomBytes = kTile * 128;
@@ -105,7 +116,6 @@ constexpr int kStages = 9;
 constexpr int kGroups = 3;             // softmax warpgroups
 constexpr int kThreads = 128 * kGroups + 96;
 constexpr int kWarpTma = 4 * kGroups, kWarpQk = kWarpTma + 1, kWarpPv = kWarpTma + 2;
-constexpr int kSeqsPerLaunch = 1024;
 
 constexpr int kXBytes = kRows * kTile * 4;                 // one half of S from the other CTA
 constexpr int kOffX = kStages * kStageBytes;               // group x's at kOffX + x * kXBytes
@@ -135,7 +145,7 @@ struct LatentParams {
   const void* query;
   const int32_t* block_tables;
   const int32_t* context_lens;
-  float* ws_o;       // [slots][H][512]
+  float* ws_o;       // [slots][H][512], 32-byte aligned
   float2* ws_ml;     // [slots][H]
   int* cum;          // [S + 1] first tile of each sequence (for the merge)
   unsigned int* err;
@@ -155,7 +165,7 @@ __device__ __forceinline__ int context_of(const LatentParams& a, int s, bool rep
   return c;
 }
 
-__device__ __forceinline__ int tiles_of(int c) { return (c + kTile - 1) / kTile; }
+__device__ __forceinline__ int tiles_of(int c) { return (int)(((unsigned)c + kTile - 1) / kTile); }
 
 // First tile of worker w of W over n tiles, and the worker of tile x.  No
 // more workers take part than there are tiles, so every one of them has some.
@@ -234,6 +244,13 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity)
     if (t0 == 0) t0 = now;
     if (now - t0 > kWaitLimitNs) return false;
   }
+}
+
+// 32 bytes in one store: a whole sector from each lane, whose rows lie apart.
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Both CTAs reach it: every wait before it is bounded.
@@ -335,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* bt = a.block_tables + (size_t)(a.seq_begin + w.cur) * a.max_blocks;
       // Block ids come 32 at a time, a lane each, with the next 32 on their way:
       // a load a tile would hold every tile's copies back by its latency.
-      const int blocks = (w.c + a.block_size - 1) / a.block_size;
+      const int blocks = (int)(((unsigned)w.c + a.block_size - 1) / a.block_size);
       int base = w.t_begin * nb;
       auto ids_from = [&](int from) { return from + lane < blocks ? bt[from + lane] : -1; };
       int ids = ids_from(base), ids_next = ids_from(base + 32);
@@ -496,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A negative multiplier's sign goes into the queries: the largest product
     // is then the largest logit.
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-    const float scale = fabsf(a.scale_log2);
+    const float scale = multiplier(a.scale_log2);
     const uint64_t scale2 = f32x2_splat(scale);
     int g = 0, seg = 0;
     bool ok = true;
@@ -718,8 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int c = 0; c < 32; c += 4)
-                *reinterpret_cast<uint4*>(prow + cb * 32 + c) = make_uint4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+              for (int c = 0; c < 32; c += 8) store32(prow + cb * 32 + c, &r[c]);
             }
           }
         }
@@ -902,13 +918,14 @@ LatentLayout latent_layout(int num_seqs, int num_heads, int sms) {
   LatentLayout l{};
   l.head_tiles = (num_heads + kRows - 1) / kRows;
   l.workers = sms / 2 / l.head_tiles > 0 ? sms / 2 / l.head_tiles : 1;
-  const int seqs = num_seqs < kSeqsPerLaunch ? num_seqs : kSeqsPerLaunch;
+  const int seqs = num_seqs < kLatentSeqsPerLaunch ? num_seqs : kLatentSeqsPerLaunch;
   const size_t slots = (size_t)seqs + l.workers;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   l.cum = 0;
   l.ml = up((size_t)(seqs + 1) * 4);
   l.o = up(l.ml + slots * num_heads * sizeof(float2));
-  l.total = up(l.o + slots * num_heads * kLatentDim * sizeof(float));
+  // 32 bytes over: the workspace is 16-byte aligned, the partials 32.
+  l.total = up(l.o + slots * num_heads * kLatentDim * sizeof(float) + 32);
   return l;
 }
 
@@ -959,7 +976,7 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
   p.context_lens = g.context_lens;
   p.cum = reinterpret_cast<int*>(g.workspace + l.cum);
   p.ws_ml = reinterpret_cast<float2*>(g.workspace + l.ml);
-  p.ws_o = reinterpret_cast<float*>(g.workspace + l.o);
+  p.ws_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(g.workspace + l.o) + 31) & ~uintptr_t(31));
   p.err = g.err;
   p.num_heads = g.num_heads;
   p.head_tiles = l.head_tiles;
@@ -970,9 +987,9 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
   p.max_context_len = g.max_context_len;
   p.oob_row = (int)rows;
   p.scale_log2 = g.scale_log2;
-  for (int b = 0; b < g.num_seqs; b += kSeqsPerLaunch) {
+  for (int b = 0; b < g.num_seqs; b += kLatentSeqsPerLaunch) {
     p.seq_begin = b;
-    p.num_seqs = g.num_seqs - b < kSeqsPerLaunch ? g.num_seqs - b : kSeqsPerLaunch;
+    p.num_seqs = g.num_seqs - b < kLatentSeqsPerLaunch ? g.num_seqs - b : kLatentSeqsPerLaunch;
     e = launch_pdl_cluster(latent_decode_kernel, dim3((unsigned)(2 * l.workers * l.head_tiles)),
                            dim3(kThreads), 2, kSmem, stream, tc, tr, p);
     if (e != cudaSuccess) return e;

@@ -58,7 +58,7 @@ namespace pa {
 namespace {
 
 constexpr int kRows = 128;    // query rows of a unit (MMA M)
-constexpr int kTile = 64;     // tokens of a tile
+constexpr int kTile = kSharedTile;  // tokens of a tile
 constexpr int kBuffers = 4;   // of S
 constexpr int kPlanThreads = 1024;
 // Members below which a prefix is not worth a pass of its own.
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
         if (in != 0 && p.leader < 0) p.leader = s0 + __ffs(in) - 1;
         members += __popc(in);
       }
-    if (members >= kMinMembers) p.tiles = (p.prefix + kTile - 1) / kTile;
+    if (members >= kMinMembers) p.tiles = (int)(((unsigned)p.prefix + kTile - 1) / kTile);
     __syncwarp();  // every lane has read the group's blocks
     if (lane == 0) {
       a.groups[g] = p;
@@ -287,10 +287,11 @@ enum {
 };
 
 // Copies of a unit's rows in the 128 lanes.
-__device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 2 : 1; }
+constexpr int kMaxCopies = 2;
+__device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? kMaxCopies : 1; }
 // First partial row of a segment.
 __device__ __forceinline__ size_t partial_row(int H, int s0, int h, int rows, int copies, int worker) {
-  return (size_t)H * s0 * 4 + (size_t)h * rows * copies + (size_t)worker * kRows;
+  return (size_t)H * s0 * kMaxCopies + (size_t)h * rows * copies + (size_t)worker * kRows;
 }
 
 // Widens one tile of codes (row-major) into the swizzled fp16 operand layout:
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
     // ---------------- softmax: one query row (of one copy) a thread
     const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
     const bool neg = a.scale_log2 < 0.f;  // then the largest logit is the smallest product
-    const float scale = fabsf(a.scale_log2);
+    const float scale = multiplier(a.scale_log2);
     const uint64_t scale2 = f32x2_splat(scale);
     auto all = [&](bool v) { return __all_sync(kFullMask, v && !*fail); };
     int g = 0, seg = 0;
@@ -791,7 +792,7 @@ struct Layout {
 Layout layout(int S, int G, int H, int D, int sms) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   Layout l{};
-  const size_t rows = (size_t)S * H * 4 + (size_t)sms * kRows;
+  const size_t rows = (size_t)S * H * kMaxCopies + (size_t)sms * kRows;
   l.total = 0;
   l.groups = 256;
   l.start = up(l.groups + (size_t)G * sizeof(GroupPlan));

@@ -309,15 +309,16 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TablesP
   const int total = a.query_start[S];
   if ((int)blockIdx.x < slot_ctas) {
     const int t0 = (int)blockIdx.x * kFillTokens;
-    const int t1 = min(t0 + kFillTokens, a.num_slots) - 1;
+    const int n = min(kFillTokens, a.num_slots - t0);
     // The sequences of the CTA's first and last token bound every search.
     if (tid < 64) {
-      const int s = last_at_most_warp(a.query_start, 0, S - 1, tid < 32 ? t0 : t1);
+      const int s = last_at_most_warp(a.query_start, 0, S - 1, tid < 32 ? t0 : t0 + n - 1);
       if ((tid & 31) == 0) range[tid >> 5] = s;
     }
     __syncthreads();
     const int lo = range[0], hi = range[1];
-    for (int t = t0 + tid; t <= t1; t += kFillThreads) {
+    for (int i = tid; i < n; i += kFillThreads) {
+      const int t = t0 + i;
       int64_t slot = -1;
       if (t < total) {
         const int s = last_at_most(a.query_start, lo, hi, t);

@@ -166,6 +166,22 @@ def test_large_logits_and_moving_maxima():
     b.check(b.run())
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-42])
+def test_a_scale_of_zero_averages_the_rows(scale):
+    b = Batch(16, [1, 31, 33, 100, 4000], 20, 16)
+    b.scale = scale
+    b.check(b.run())
+
+
+def test_a_workspace_on_any_16_bytes():
+    b = Batch(17, [3000, 40, 2000], 48, 16)
+    n = pa.pa_latent_decode_workspace_size(b.S, b.H)
+    for at in (16, 32, 48):
+        buf = torch.full((n + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+        b.check(b.run(ws=buf[at:at + n]))
+        assert bool((buf[:at] == 0xA5).all()) and bool((buf[at + n:] == 0xA5).all())
+
+
 def test_a_row_of_infinite_logits_stays_in_its_row():
     b = Batch(4, [100, 100], 16, 16)
     b.q[0, 3] = float("inf")

@@ -206,6 +206,13 @@ def test_growing_logits_move_the_reference():
     b.check(b.run())
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp16", "fp8"])
+def test_a_scale_of_zero_averages_the_values(fp8):
+    b = Batch(31, [3, 40], [5, 9], [0, 3, 30], 3, 128, 16, fp8, lone=1)
+    b.scale = 0.0
+    b.check(b.run())
+
+
 def test_infinite_logits_of_one_member_stay_in_its_row():
     b = Batch(26, [10], [30], [20], 2, 128, 16)
     b.q[4, 1] = float("inf")

@@ -44,7 +44,8 @@ TABLES = dict(block_tables=P[0], max_blocks=8, context=P[1], query_start=P[2], s
     (dict(cached=None), INVALID), (dict(new=P[8] + 1), INVALID), (dict(group_start=None), INVALID),
     (dict(prefix=None), INVALID), (dict(ws=None), INVALID), (dict(ws=P[11] + 8), INVALID),
     (dict(ws_bytes=64), INVALID), (dict(context=P[8]), INVALID), (dict(query_start=P[7]), INVALID),
-    (dict(free_out=P[5]), INVALID), (dict(block_tables=P[5]), INVALID), (dict(seqs=1 << 20, max_blocks=1 << 12,
+    (dict(free_out=P[5]), INVALID), (dict(block_tables=P[5]), INVALID), (dict(context=P[2]), INVALID),
+    (dict(slots=P[0]), INVALID), (dict(slots=P[8]), INVALID), (dict(free_out=P[1]), INVALID), (dict(seqs=1 << 20, max_blocks=1 << 12,
                                                                               ws_bytes=1 << 30), UNSUPPORTED),
 ])
 def test_build_tables_refusals(lib, change, status):
@@ -62,7 +63,8 @@ DECODE = dict(out=P[0], q=P[1], cache=P[2], bt=P[3], max_blocks=4, ctx=P[4], seq
     (dict(seqs=-1), INVALID), (dict(num_blocks=0), INVALID), (dict(max_blocks=0), INVALID),
     (dict(max_len=-1), INVALID), (dict(out=None), INVALID), (dict(q=P[1] + 8), INVALID),
     (dict(cache=P[2] + 2), INVALID), (dict(bt=P[3] + 2), INVALID), (dict(ws=None), INVALID),
-    (dict(ws_bytes=1000), INVALID), (dict(num_blocks=1 << 28), UNSUPPORTED), (dict(seqs=0, out=None), OK),
+    (dict(ws_bytes=1000), INVALID), (dict(num_blocks=1 << 28), UNSUPPORTED),
+    (dict(seqs=1024, max_blocks=1 << 27, max_len=2 ** 31 - 1), UNSUPPORTED), (dict(seqs=0, out=None), OK),
 ])
 def test_latent_decode_refusals(lib, change, status):
     assert lib.pa_latent_decode(*dict(DECODE, **change).values()) == status
@@ -93,7 +95,8 @@ SHARED_TAIL = dict(max_len=100, max_prefix=32, ws=P[8], ws_bytes=1 << 34, stream
     (dict(bt=P[4] + 1), INVALID), (dict(ctx=None), INVALID), (dict(starts=None), INVALID),
     (dict(pre=P[7] + 2), INVALID), (dict(ws=None), INVALID), (dict(ws=P[8] + 8), INVALID),
     (dict(ws_bytes=1 << 10), INVALID), (dict(num_blocks=1 << 24), UNSUPPORTED),
-    (dict(max_prefix=2 ** 31 - 1, heads=128), UNSUPPORTED), (dict(seqs=0, out=None), OK),
+    (dict(max_prefix=2 ** 31 - 1, heads=128), UNSUPPORTED),
+    (dict(max_prefix=600_000_000, heads=128), UNSUPPORTED),   # 2^31 tiles of 64 tokens (dict(seqs=0, out=None), OK),
 ])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_decode_shared_refusals(lib, fp8, change, status):
