@@ -84,6 +84,19 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity)
   return true;
 }
 
+// The same by a whole (converged) warp, with one result for all: true when
+// every lane sees the phase complete, false on timeout or once *fail is set.
+// The test and a vote are all that a wait costs that ends at once; a vote
+// behind every lane's own loop makes it 123 cycles, one that reads *fail 199.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const volatile int* fail) {
+  if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!__all_sync(kFullMask, mbar_try_wait(bar, parity))) {
+    if (__any_sync(kFullMask, *fail != 0 || global_timer_ns() - t0 > kWaitLimitNs)) return false;
+  }
+  return true;
+}
+
 // ---- 1-D bulk copy global -> shared, completing on an mbarrier ----------
 // Both addresses 16-byte aligned, bytes a multiple of 16.
 

@@ -225,25 +225,27 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Bounded wait on a barrier that the other CTA completes.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint64_t t0 = 0;
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n"
-        "  .reg .pred p;\n"
-        "  mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        "  selp.u32 %0, 1, 0, p;\n"
-        "}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    const uint64_t now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitLimitNs) return false;
+// mbar_wait_warp on a barrier that the other CTA completes.
+__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "  selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const volatile int* fail) {
+  if (__all_sync(kFullMask, mbar_test_cluster(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!__all_sync(kFullMask, mbar_test_cluster(bar, parity))) {
+    if (__any_sync(kFullMask, *fail != 0 || global_timer_ns() - t0 > kWaitLimitNs)) return false;
   }
+  return true;
 }
 
 // 32 bytes in one store: a whole sector from each lane, whose rows lie apart.
@@ -508,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t x_bytes = (uint32_t)live_warps * 32 * kTile * 4;
     float* ref_s = reinterpret_cast<float*>(sm + kOffRef) + row;
     float2* ml_s = reinterpret_cast<float2*>(sm + kOffMl) + row;
-    auto all = [&](bool v) { return __all_sync(kFullMask, v && !*fail); };
+    auto wait = [&](int b, uint32_t parity) { return mbar_wait_warp(bar(b), parity, fail); };
     if (row == 0 && x < n_tiles) mbar_arrive_expect_tx(bar(kXFull + x), x_bytes);
     // A negative multiplier's sign goes into the queries: the largest product
     // is then the largest logit.
@@ -566,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int px = (g + 2) % 3;  // the group of the tile before, and that tile's phase
         const uint32_t ppar = ((g - 1) / 3) & 1;
         const bool first = t == w.t_begin;
-        ok = all(mbar_wait_bounded(bar(kSFull + x), par));
+        ok = wait(kSFull + x, par);
         if (!ok) break;
         uint32_t sr[kTile];
         if (live) {
@@ -581,12 +583,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool rescale = false;
         if (live) {
           // This CTA's half of the logits to the other one; the other's half.
-          ok = g < 3 || all(mbar_wait_cluster(bar(kXFree + x), par ^ 1));
+          ok = g < 3 || mbar_wait_cluster(bar(kXFree + x), par ^ 1, fail);
           if (!ok) break;
 #pragma unroll
           for (int c = 0; c < kTile / 4; ++c)
             send16(x_peer + c * (kRows * 16), x_full_peer, sr[4 * c], sr[4 * c + 1], sr[4 * c + 2], sr[4 * c + 3]);
-          ok = all(mbar_wait_cluster(bar(kXFull + x), par));
+          ok = mbar_wait_cluster(bar(kXFull + x), par, fail);
           if (!ok) break;
           float y[kTile];
 #pragma unroll
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // The reference after the tile before.
           float before = -INFINITY;
           if (!first) {
-            ok = all(mbar_wait_bounded(bar(kRef + px), ppar));
+            ok = wait(kRef + px, ppar);
             if (!ok) break;
             before = *ref_s;
           }
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = ref;
         } else {
           if (!first) {
-            ok = all(mbar_wait_bounded(bar(kRef + px), ppar));
+            ok = wait(kRef + px, ppar);
             if (!ok) break;
           }
           mbar_arrive(bar(kRef + x));
@@ -660,12 +662,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // This group's P is free once P.V of its tile before is done; O may be
         // rescaled once that of the other group's is, too.
-        ok = g < 3 || all(mbar_wait_bounded(bar(kOFull + x), par ^ 1));
+        ok = g < 3 || wait(kOFull + x, par ^ 1);
         if (!ok) break;
         if (live) {
           tc_fence_after();
           if (!first && rescale) {
-            ok = all(mbar_wait_bounded(bar(kOFull + px), ppar));
+            ok = wait(kOFull + px, ppar);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1  // seldom taken: unrolled, it costs the loop its registers
@@ -689,13 +691,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The groups' references and sums, joined at the last reference.
       ml_s[x * kRows] = make_float2(m, l);
       mbar_arrive(bar(kSegA));
-      ok = all(mbar_wait_bounded(bar(kSegA), seg & 1));
+      ok = wait(kSegA, seg & 1);
       if (!ok) break;
       // Every S of the segment has been taken, so its products with the queries
       // are done: the next segment's first ones run beside this one's epilogue.
       if (more) load_queries(ahead);
       const int last = g - 1;
-      ok = all(mbar_wait_bounded(bar(kOFull + last % 3), (last / 3) & 1));
+      ok = wait(kOFull + last % 3, (last / 3) & 1);
       if (!ok) break;
       // The segment's output, a third of it by each group: to `out` when it is the
       // whole sequence, else a partial.
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Both groups have read O and the sums before the next segment's are written.
       mbar_arrive(bar(kSegB));
-      ok = all(mbar_wait_bounded(bar(kSegB), seg & 1));
+      ok = wait(kSegB, seg & 1);
       ++seg;
     }
     if (!ok && lane == 0) *fail = 1;

@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
     const bool neg = a.scale_log2 < 0.f;  // then the largest logit is the smallest product
     const float scale = multiplier(a.scale_log2);
     const uint64_t scale2 = f32x2_splat(scale);
-    auto all = [&](bool v) { return __all_sync(kFullMask, v && !*fail); };
+    auto wait = [&](int b, uint32_t parity) { return mbar_wait_warp(bar(b), parity, fail); };
     int g = 0, seg = 0;
     bool ok = true;
     // The queries of a segment to tensor memory, a segment ahead (the place was
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
       float m = -INFINITY, l = 0.f;
       for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
         const uint32_t t_s = tmem + t_lane + kTile * (g & 3);
-        ok = all(mbar_wait_bounded(bar(kSFull + (g & 3)), (g >> 2) & 1));
+        ok = wait(kSFull + (g & 3), (g >> 2) & 1);
         if (!ok) break;
         if (live) {
           tc_fence_after();
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
             l = l * alpha + ((sq[0] + sq[1]) + (sq[2] + sq[3]));
             if (t > w.t_begin && __any_sync(kFullMask, alpha != 1.f)) {
               // O holds the tiles up to t - 1 once P.V of t - 1 is done.
-              ok = all(mbar_wait_bounded(bar(kOFull + ((g - 1) & 3)), ((g - 1) >> 2) & 1));
+              ok = wait(kOFull + ((g - 1) & 3), ((g - 1) >> 2) & 1);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
       }
       if (!ok) break;
       // The segment's partial rows.
-      ok = all(mbar_wait_bounded(bar(kOFull + ((g - 1) & 3)), ((g - 1) >> 2) & 1));
+      ok = wait(kOFull + ((g - 1) & 3), ((g - 1) >> 2) & 1);
       if (!ok) break;
       if (live) {
         tc_fence_after();
@@ -685,9 +685,8 @@ __global__ void __launch_bounds__(Traits<D, F8>::THREADS, 1)
     while (ok && w.next(a)) {
       for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
         const int cs = g % NCS, st = g % NST;
-        ok = mbar_wait_bounded(bar(kCFull + 4 * kv + cs), (g / NCS) & 1);
-        if (g >= NST) ok = ok && mbar_wait_bounded(bar((kv ? kVEmpty : kKEmpty) + st), (g / NST - 1) & 1);
-        ok = __all_sync(kFullMask, ok && !*fail);
+        ok = mbar_wait_warp(bar(kCFull + 4 * kv + cs), (g / NCS) & 1, fail);
+        if (g >= NST) ok = ok && mbar_wait_warp(bar((kv ? kVEmpty : kKEmpty) + st), (g / NST - 1) & 1, fail);
         if (!ok) break;
         widen<D>(sm + T::OFF_C + (NCS * kv + cs) * T::CB, sm + (kv ? T::OFF_V : 0) + st * T::TB, i);
         fence_proxy_async_smem();
