@@ -142,7 +142,6 @@ enum {
 
 struct LatentParams {
   void* out;
-  const void* query;
   const int32_t* block_tables;
   const int32_t* context_lens;
   float* ws_o;       // [slots][H][512], 32-byte aligned
@@ -263,6 +262,7 @@ __device__ __forceinline__ void cluster_sync() {
 
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap tc, const __grid_constant__ CUtensorMap tr,
+                         const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tqr,
                          const LatentParams a) {
   extern __shared__ __align__(1024) unsigned char sm[];  // the swizzle's phase is the address's
   const uint32_t s_base = smem_u32(sm);
@@ -289,6 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     prefetch_tensormap(&tc);
     prefetch_tensormap(&tr);
+    prefetch_tensormap(&tq);
+    prefetch_tensormap(&tqr);
   }
   if (warp == kWarpTma) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -345,12 +347,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_tiles = w.left;
 
   if (warp == kWarpTma) {
-    // ---------------- TMA: the tiles of the range
+    // ---------------- TMA: each segment's queries, 32 heads a stage, and its tiles
     const int nb = kTile / a.block_size;
     const int b = lane & (nb - 1);
-    int g = 0;
+    int g = 0;  // stages filled
     bool ok = true;
     while (ok && w.next(a)) {
+      for (int i = 0; ok && i < live_warps; ++i) {
+        const int st = g % kStages;
+        bool mine = true;
+        if (elect_one()) {
+          mine = g < kStages || mbar_wait_bounded(bar(kKEmpty + st), (g / kStages - 1) & 1);
+          if (mine) {
+            mbar_arrive_expect_tx(bar(kKFull + st), kStageBytes);
+            const uint32_t dst = s_base + st * kStageBytes;
+            const int from = (a.seq_begin + w.cur) * a.num_heads + h0 + 32 * i;
+#pragma unroll
+            for (int at = 0; at < kAtoms; ++at)
+              tma_load_2d(dst + at * kAtomBytes, &tq, (int)rank * kHalf + at * 64, from, bar(kKFull + st));
+            tma_load_2d(dst + kAtoms * kAtomBytes, &tqr, kLatentDim + (int)rank * (kRopeDim / 2), from,
+                        bar(kKFull + st));
+          }
+        }
+        ok = __all_sync(kFullMask, mine);
+        if (ok) ++g;
+      }
+      if (!ok) break;
       const int32_t* bt = a.block_tables + (size_t)(a.seq_begin + w.cur) * a.max_blocks;
       // Block ids come 32 at a time, a lane each, with the next 32 on their way:
       // a load a tile would hold every tile's copies back by its latency.
@@ -424,6 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           left = w.t_end - w.t_begin;
           ok = mbar_wait_bounded(bar(kQFull), seg & 1);
           ++seg;
+          // The queries are in tensor memory: their stages are free.
+          for (int q = 0; ok && q < live_warps; ++q) {
+            mbar_arrive(bar(kKEmpty + st));
+            if (++st == kStages) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
         }
         --left;
         // S(i) takes the place of S(i - 2), once that is in registers; the tile.
@@ -470,6 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (first) {
           w.next(a);
           left = w.t_end - w.t_begin;
+          st += live_warps;  // past the segment's queries
+          if (st >= kStages) st -= kStages;
         }
         --left;
         ok = mbar_wait_bounded(bar(kPFull + g3), ph3);
@@ -519,44 +551,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t scale2 = f32x2_splat(scale);
     int g = 0, seg = 0;
     bool ok = true;
-    // The queries of a segment to tensor memory, some by each group.  Rows past
-    // the heads are zero.
-    auto load_queries = [&](const Walk& n) {
+    // The queries of a segment from their stages to tensor memory, some by each
+    // group.  `at`: the stages filled before them.  (Rows past the heads hold
+    // what follows in memory, or zeros at its end; nothing reads their results.)
+    auto load_queries = [&](int at) {
       if (live) {
-        const __half* q = static_cast<const __half*>(a.query) +
-                          ((size_t)(a.seq_begin + n.cur) * a.num_heads + (h < a.num_heads ? h : 0)) * kLatentRow;
-        // Columns 32 cb to 32 cb + 31: groups 0 and 1 two of the four each, group
-        // 2 the rotary 16.
-        auto load = [&](const __half* from, uint32_t (&r)[32], int vecs) {
-          const uint4* src = reinterpret_cast<const uint4*>(from);
+        const int u = at + (warp & 3), st = u % kStages;
+        if (!wait(kKFull + st, (u / kStages) & 1)) return false;
+        const unsigned char* q = sm + st * kStageBytes + lane * 128;
+        // 16-byte vector v of the row's part in an atom, as the copy swizzled it.
+        auto load = [&](const unsigned char* from, int swizzle, int vecs, uint32_t (&r)[32]) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const uint4 v = c < vecs && h < a.num_heads ? src[c] : make_uint4(0, 0, 0, 0);
+            if (c >= vecs) break;
+            const uint4 v = lds128(from + ((c ^ swizzle) << 4));
             r[4 * c] = v.x ^ flip;
             r[4 * c + 1] = v.y ^ flip;
             r[4 * c + 2] = v.z ^ flip;
             r[4 * c + 3] = v.w ^ flip;
           }
         };
+        // Columns 32 cb to 32 cb + 31: groups 0 and 1 two of the four each, group
+        // 2 the rotary 16.
         uint32_t r[32];
         if (x < 2) {
 #pragma unroll 1
           for (int cb = 2 * x; cb < 2 * x + 2; ++cb) {
-            load(q + rank * kHalf + cb * 64, r, 8);
+            load(q + cb * kAtomBytes, lane & 7, 8, r);
             tmem_st32(tmem + t_lane + kColQ + 32 * cb, r);
           }
         } else {
-          load(q + kLatentDim + rank * (kRopeDim / 2), r, 4);
+          // Rows of 64 bytes: two share a line of 128.
+          load(sm + st * kStageBytes + kAtoms * kAtomBytes + lane * 64, (lane >> 1) & 3, 4, r);
           tmem_st16(tmem + t_lane + kColQ + 128, *reinterpret_cast<const uint32_t(*)[16]>(&r[0]));
         }
         tmem_wait_st();
         tc_fence_before();
       }
       mbar_arrive(bar(kQFull));
+      return true;
     };
     Walk ahead = w;
     bool more = ahead.next(a);
-    if (more) load_queries(ahead);
+    if (more) ok = load_queries(0);
     while (ok && more) {
       w = ahead;
       more = ahead.next(a);
@@ -651,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
           const int left = w.c - t * kTile;
           if (left < kTile) {
-            unsigned char* v = sm + (g % kStages) * kStageBytes;
+            unsigned char* v = sm + ((g + (seg + 1) * live_warps) % kStages) * kStageBytes;
             const int chunks = (kTile - left) * 8;
             for (int q = row; q < chunks * kAtoms; q += 128) {
               const int at = q / chunks, rr = left + (q % chunks) / 8, ch = q % 8;
@@ -695,9 +732,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // Every S of the segment has been taken, so its products with the queries
       // are done: the next segment's first ones run beside this one's epilogue.
-      if (more) load_queries(ahead);
+      if (more) ok = load_queries(g + (seg + 1) * live_warps);
       const int last = g - 1;
-      ok = wait(kOFull + last % 3, (last / 3) & 1);
+      ok = ok && wait(kOFull + last % 3, (last / 3) & 1);
       if (!ok) break;
       // The segment's output, a third of it by each group: to `out` when it is the
       // whole sequence, else a partial.
@@ -963,17 +1000,20 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
   }
   const LatentLayout l = latent_layout(g.num_seqs, g.num_heads, g.sms);
   const long long rows = (long long)g.num_blocks * g.block_size;
-  CUtensorMap tc, tr;
+  CUtensorMap tc, tr, tq, tqr;
   const cuuint64_t str[1] = {(cuuint64_t)kLatentRow * 2};
   const cuuint64_t cdims[2] = {(cuuint64_t)kLatentRow, (cuuint64_t)rows};
   const cuuint32_t cbox[2] = {64, (cuuint32_t)g.block_size};
   const cuuint32_t rbox[2] = {kRopeDim / 2, (cuuint32_t)g.block_size};
+  const cuuint64_t qdims[2] = {(cuuint64_t)kLatentRow, (cuuint64_t)g.num_seqs * g.num_heads};
+  const cuuint32_t qbox[2] = {64, kTile}, qrbox[2] = {kRopeDim / 2, kTile};
   if (!encode_tensor_map(&tc, g.cache, 2, cdims, str, cbox) ||
+      !encode_tensor_map(&tq, g.query, 2, qdims, str, qbox) ||
+      !encode_tensor_map(&tqr, g.query, 2, qdims, str, qrbox, false, CU_TENSOR_MAP_SWIZZLE_64B) ||
       !encode_tensor_map(&tr, g.cache, 2, cdims, str, rbox, false, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   LatentParams p{};
   p.out = g.out;
-  p.query = g.query;
   p.block_tables = g.block_tables;
   p.context_lens = g.context_lens;
   p.cum = reinterpret_cast<int*>(g.workspace + l.cum);
@@ -993,7 +1033,7 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
     p.seq_begin = b;
     p.num_seqs = g.num_seqs - b < kLatentSeqsPerLaunch ? g.num_seqs - b : kLatentSeqsPerLaunch;
     e = launch_pdl_cluster(latent_decode_kernel, dim3((unsigned)(2 * l.workers * l.head_tiles)),
-                           dim3(kThreads), 2, kSmem, stream, tc, tr, p);
+                           dim3(kThreads), 2, kSmem, stream, tc, tr, tq, tqr, p);
     if (e != cudaSuccess) return e;
     const long long pairs = (long long)p.num_seqs * p.num_heads;
     e = p.num_seqs < l.workers / 4
