@@ -144,7 +144,7 @@ struct LatentParams {
   void* out;
   const int32_t* block_tables;
   const int32_t* context_lens;
-  float* ws_o;       // [slots][H][512], 32-byte aligned
+  float* ws_o;       // [slots][ceil(H / 32)][64][32 heads][8 values], 32-byte aligned
   float2* ws_ml;     // [slots][H]
   int* cum;          // [S + 1] first tile of each sequence (for the merge)
   unsigned int* err;
@@ -175,6 +175,7 @@ __device__ __forceinline__ int worker_begin(int w, int W, int n) {
   return (int)((long long)w * n / W);
 }
 __device__ __forceinline__ int worker_of(int x, int W, int n) {
+  if (n < (1 << 24)) return (int)((((unsigned)x + 1) * (unsigned)W - 1) / (unsigned)n);  // W < 256
   return (int)((((long long)x + 1) * W - 1) / n);
 }
 
@@ -247,11 +248,24 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
   return true;
 }
 
-// 32 bytes in one store: a whole sector from each lane, whose rows lie apart.
+// Where a partial's values [8 chunk, 8 chunk + 8) of head h are.  32 heads of a
+// chunk lie together, so that a warp with a head a lane writes whole lines (a
+// row a head: a line a lane and store, 2.9 us for 128 heads instead of 2.3).
+__device__ __forceinline__ size_t partial_at(const LatentParams& a, int slot, int h, int chunk) {
+  const int blocks = (a.num_heads + 31) / 32;
+  return (((size_t)slot * blocks + (h >> 5)) * (kLatentDim / 8) + chunk) * 256 + (h & 31) * 8;
+}
+
+// 32 bytes in one store, or one load.
 __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+__device__ __forceinline__ void load32(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p));
 }
 
 // Both CTAs reach it: every wait before it is bounded.
@@ -353,6 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;  // stages filled
     bool ok = true;
     while (ok && w.next(a)) {
+      const int32_t* bt = a.block_tables + (size_t)(a.seq_begin + w.cur) * a.max_blocks;
+      // Block ids come 32 at a time, a lane each, with the next 32 on their way:
+      // a load a tile would hold every tile's copies back by its latency.
+      const int blocks = (int)(((unsigned)w.c + a.block_size - 1) / a.block_size);
+      int base = w.t_begin * nb;
+      auto ids_from = [&](int from) { return from + lane < blocks ? bt[from + lane] : -1; };
+      int ids = ids_from(base), ids_next = ids_from(base + 32);
       for (int i = 0; ok && i < live_warps; ++i) {
         const int st = g % kStages;
         bool mine = true;
@@ -373,13 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ++g;
       }
       if (!ok) break;
-      const int32_t* bt = a.block_tables + (size_t)(a.seq_begin + w.cur) * a.max_blocks;
-      // Block ids come 32 at a time, a lane each, with the next 32 on their way:
-      // a load a tile would hold every tile's copies back by its latency.
-      const int blocks = (int)(((unsigned)w.c + a.block_size - 1) / a.block_size);
-      int base = w.t_begin * nb;
-      auto ids_from = [&](int from) { return from + lane < blocks ? bt[from + lane] : -1; };
-      int ids = ids_from(base), ids_next = ids_from(base + 32);
       for (int t = w.t_begin; t < w.t_end; ++t, ++g) {
         const int st = g % kStages;
         if (t * nb - base >= 32) {
@@ -753,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t ph = (size_t)(w.cur + worker) * a.num_heads + h;
         if (!whole && rank == 0 && x == 0 && h < a.num_heads) a.ws_ml[ph] = make_float2(m, l);
         __half* orow = static_cast<__half*>(a.out) + sh * kLatentDim + rank * kHalf;
-        float* prow = a.ws_o + ph * kLatentDim + rank * kHalf;
+        float* prow = a.ws_o + partial_at(a, w.cur + worker, h, rank * (kHalf / 8));
 #pragma unroll 1
         for (int cb = x; cb < kHalf / 32; cb += kGroups) {
           uint32_t r[32];
@@ -774,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int c = 0; c < 32; c += 8) store32(prow + cb * 32 + c, &r[c]);
+              for (int c = 0; c < 4; ++c) store32(prow + (4 * cb + c) * 256, &r[8 * c]);
             }
           }
         }
@@ -802,150 +816,111 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the segments of each (sequence, head): with M = max m_i,
 //   out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
 // A sequence of no tokens gets zeros, one that a single worker covered is
-// already written.  Two forms, by the batch's shape alone (the order of the
-// sums is part of the result): many sequences have few segments each, and a
-// warp takes a pair; of few sequences each has many segments, and a CTA takes a
-// pair, its groups of 128 threads the segments in turn.  (64 sequences of
-// 4096-8192 tokens, 128 heads: 25 us by CTAs; two of 60-100 thousand tokens, 64
-// heads: 19 us with one group, 3 us with four.)
+// already written.  A warp takes 4 heads and 64 values of a sequence, a lane
+// one head's 8 values: as the partials lie, 128 bytes of 8 lines a load.  The
+// latency of few dependent loads bounds it, so a warp has kAhead segments'
+// partials on their way at a time, and the maximum is a running one.  Two
+// forms, by the batch's shape alone (the order of the sums is part of the
+// result): many sequences have few segments each, and a warp takes them all;
+// of few sequences each has many, and the warps of a CTA take them in turn.
+constexpr int kAhead = 4;
 
-// Where the partials of pair (s, h) are; false: nothing to join.
-__device__ __forceinline__ bool merge_segments(const LatentParams& a, int s, int h, bool* empty, size_t* base, int* n) {
+template <int GROUPS>  // warps that share a sequence's segments
+__global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) latent_merge_kernel(const LatentParams a) {
+  constexpr int kParts = kLatentDim / 64;
+  __shared__ float2 ml_s[GROUPS][GROUPS == 1 ? 1 : 32];
+  __shared__ float o_s[GROUPS][GROUPS == 1 ? 1 : 32][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int quads = (a.num_heads + 3) / 4;
+  const int task = GROUPS == 1 ? (int)blockIdx.x * 4 + warp : (int)blockIdx.x;
+  const int group = GROUPS == 1 ? 0 : warp;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (task >= a.num_seqs * quads * kParts) return;
+  const int part = task % kParts, s = task / kParts / quads, quad = task / kParts - s * quads;
   const int c0 = a.cum[s], c1 = a.cum[s + 1], total = a.cum[a.num_seqs];
-  *empty = c0 == c1;
-  if (*empty) return false;
-  const int W = active_workers(a, total);
-  const int w0 = worker_of(c0, W, total), w1 = worker_of(c1 - 1, W, total);
-  *n = w1 - w0 + 1;
-  *base = (size_t)(s + w0) * a.num_heads + h;
-  return *n > 1;
-}
-
-__device__ __forceinline__ uint2 half4(const float4& v, float inv) {
-  const __half2 x = __floats2half2_rn(v.x * inv, v.y * inv), y = __floats2half2_rn(v.z * inv, v.w * inv);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-}
-
-__device__ __forceinline__ void fma4(float4& o, float x, const float4& v) {
-  o.x = fmaf(x, v.x, o.x);
-  o.y = fmaf(x, v.y, o.y);
-  o.z = fmaf(x, v.z, o.z);
-  o.w = fmaf(x, v.w, o.w);
-}
-
-// A warp a pair: lane l has values 4 l + 128 j, j < 4.
-__global__ void __launch_bounds__(128) latent_merge_warp_kernel(const LatentParams a) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long long pair = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (pair >= (long long)a.num_seqs * a.num_heads) return;
-  const int s = (int)(pair / a.num_heads), h = (int)(pair - (long long)s * a.num_heads);
-  __half* out = static_cast<__half*>(a.out) + ((size_t)(a.seq_begin + s) * a.num_heads + h) * kLatentDim + 4 * lane;
-  bool empty;
-  size_t base;
-  int n;
-  if (!merge_segments(a, s, h, &empty, &base, &n)) {
-    if (empty)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint2*>(out + 128 * j) = make_uint2(0, 0);
-    return;
-  }
-  const float2* ml = a.ws_ml + base;
-  const float* src = a.ws_o + base * kLatentDim + 4 * lane;
-  const size_t step = (size_t)a.num_heads * kLatentDim;
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[(size_t)i * a.num_heads].x);
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-  float L = 0.f;
-  float4 o[4] = {};
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float wt = 0.f;
-    if (i0 + lane < n) {
-      const float2 x = ml[(size_t)(i0 + lane) * a.num_heads];
-      wt = x.x == -INFINITY ? 0.f : exp2_approx(x.x - M);
-      L = fmaf(wt, x.y, L);
-    }
-    const int cnt = min(32, n - i0);
-#pragma unroll 2
-    for (int i = 0; i < cnt; ++i) {
-      const float x = __shfl_sync(kFullMask, wt, i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        fma4(o[j], x, *reinterpret_cast<const float4*>(src + (i0 + i) * step + 128 * j));
-    }
-  }
-#pragma unroll
-  for (int k = 16; k >= 1; k >>= 1) L += __shfl_xor_sync(kFullMask, L, k);
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint2*>(out + 128 * j) = half4(o[j], inv);
-}
-
-constexpr int kMergeGroups = 4;
-constexpr int kMergeChunk = 128;  // segments whose weights are held at a time
-
-__global__ void __launch_bounds__(128 * kMergeGroups) latent_merge_kernel(const LatentParams a) {
-  __shared__ float wt_s[kMergeChunk];
-  __shared__ float red[16];
-  __shared__ float4 part[kMergeGroups - 1][128];
-  pdl_wait();
-  pdl_launch_dependents();
-  constexpr int groups = kMergeGroups, warps = 4 * kMergeGroups;
-  const int tid = threadIdx.x, group = tid >> 7, d4 = tid & 127;
-  const int warp = tid >> 5, lane = tid & 31;
-  const int s = (int)blockIdx.x / a.num_heads, h = (int)blockIdx.x - s * a.num_heads;
-  __half* out = static_cast<__half*>(a.out) +
-                ((size_t)(a.seq_begin + s) * a.num_heads + h) * kLatentDim + 4 * d4;
-  bool empty;
-  size_t base;
-  int n;
-  if (!merge_segments(a, s, h, &empty, &base, &n)) {
-    if (empty && group == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
-    return;
-  }
-  auto block_max = [&](float v) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    for (int i = 0; i < warps; ++i) v = fmaxf(v, red[i]);
-    __syncthreads();
-    return v;
+  auto address = [&](int l) {  // of lane l's output
+    const size_t sh = (size_t)(a.seq_begin + s) * a.num_heads + 4 * quad + (l & 3);
+    return static_cast<__half*>(a.out) + sh * kLatentDim + part * 64 + (l >> 2) * 8;
   };
-  float M = -INFINITY;
-  for (int i = tid; i < n; i += 128 * kMergeGroups) M = fmaxf(M, a.ws_ml[base + (size_t)i * a.num_heads].x);
-  M = block_max(M);
-  float L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += kMergeChunk) {
-    const int cnt = min(kMergeChunk, n - i0);
-    if (tid < cnt) {
-      const float2 ml = a.ws_ml[base + (size_t)(i0 + tid) * a.num_heads];
-      const float wt = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - M);
-      wt_s[tid] = wt;
-      L = fmaf(wt, ml.y, L);
-    }
-    __syncthreads();
-    const float* src = a.ws_o + (base + (size_t)i0 * a.num_heads) * kLatentDim + 4 * d4;
-    const size_t step = (size_t)a.num_heads * kLatentDim;
-#pragma unroll 8
-    for (int i = group; i < cnt; i += groups) {
-      fma4(o, wt_s[i], *reinterpret_cast<const float4*>(src + i * step));
-    }
-    __syncthreads();
+  const int h = 4 * quad + (lane & 3);
+  const bool live = h < a.num_heads;
+  if (c0 == c1) {
+    if (live && group == 0) *reinterpret_cast<uint4*>(address(lane)) = make_uint4(0, 0, 0, 0);
+    return;
   }
-  if (group > 0) part[group - 1][d4] = o;
+  const int W = active_workers(a, total);
+  const int w0 = worker_of(c0, W, total), n = worker_of(c1 - 1, W, total) - w0 + 1;
+  if (n <= 1) return;
+  const size_t step_ml = a.num_heads, step_o = partial_at(a, 1, 0, 0);
+  const float2* ml = a.ws_ml + (size_t)(s + w0) * a.num_heads + h;
+  const float* src = a.ws_o + partial_at(a, s + w0, h, part * 8 + (lane >> 2));
+  float M = -INFINITY, L = 0.f, o[8] = {};
+  for (int i0 = group; i0 < n; i0 += kAhead * GROUPS) {
+    float2 x[kAhead];
+    float v[kAhead][8];
 #pragma unroll
-  for (int k = 16; k >= 1; k >>= 1) L += __shfl_xor_sync(kFullMask, L, k);
-  if (lane == 0) red[warp] = L;
-  __syncthreads();
-  if (group > 0) return;
-  L = 0.f;
-  for (int i = 0; i < warps; ++i) L += red[i];
-  for (int i = 0; i + 1 < groups; ++i) fma4(o, 1.f, part[i][d4]);
-  *reinterpret_cast<uint2*>(out) = half4(o, L > 0.f ? 1.f / L : 0.f);
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * GROUPS;
+      x[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[u][k] = 0.f;
+      if (live && i < n) {
+        x[u] = ml[i * step_ml];
+        load32(src + i * step_o, v[u]);
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) top = fmaxf(top, x[u].x);
+    const float keep = M == -INFINITY ? 0.f : exp2_approx(M - top);
+    M = top;
+    L *= keep;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] *= keep;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const float wt = x[u].x == -INFINITY ? 0.f : exp2_approx(x[u].x - top);
+      L = fmaf(wt, x[u].y, L);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = fmaf(wt, v[u][k], o[k]);
+    }
+  }
+  if constexpr (GROUPS == 1) {
+    if (!live) return;
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    uint32_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __half2 y = __floats2half2_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
+      r[k] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    *reinterpret_cast<uint4*>(address(lane)) = make_uint4(r[0], r[1], r[2], r[3]);
+  } else {
+    ml_s[group][lane] = make_float2(M, L);
+#pragma unroll
+    for (int k = 0; k < 8; k += 4)
+      *reinterpret_cast<float4*>(&o_s[group][lane][k]) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+    __syncthreads();
+    // Two values of one lane's eight a thread.
+    const int l = (int)threadIdx.x >> 2, k = 2 * (threadIdx.x & 3);
+    if (l >= 32 || 4 * quad + (l & 3) >= a.num_heads) return;
+    M = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) M = fmaxf(M, ml_s[g][l].x);
+    L = 0.f;
+    float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      const float2 x = ml_s[g][l];
+      const float wt = x.x == -INFINITY ? 0.f : exp2_approx(x.x - M);
+      L = fmaf(wt, x.y, L);
+      y0 = fmaf(wt, o_s[g][l][k], y0);
+      y1 = fmaf(wt, o_s[g][l][k + 1], y1);
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    *reinterpret_cast<__half2*>(address(l) + k) = __floats2half2_rn(y0 * inv, y1 * inv);
+  }
 }
 
 struct LatentLayout {
@@ -963,8 +938,9 @@ LatentLayout latent_layout(int num_seqs, int num_heads, int sms) {
   l.cum = 0;
   l.ml = up((size_t)(seqs + 1) * 4);
   l.o = up(l.ml + slots * num_heads * sizeof(float2));
+  const size_t rows = (size_t)(num_heads + 31) / 32 * 32;
   // 32 bytes over: the workspace is 16-byte aligned, the partials 32.
-  l.total = up(l.o + slots * num_heads * kLatentDim * sizeof(float) + 32);
+  l.total = up(l.o + slots * rows * kLatentDim * sizeof(float) + 32);
   return l;
 }
 
@@ -1035,10 +1011,10 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
     e = launch_pdl_cluster(latent_decode_kernel, dim3((unsigned)(2 * l.workers * l.head_tiles)),
                            dim3(kThreads), 2, kSmem, stream, tc, tr, tq, tqr, p);
     if (e != cudaSuccess) return e;
-    const long long pairs = (long long)p.num_seqs * p.num_heads;
+    const unsigned tasks = (unsigned)p.num_seqs * ((p.num_heads + 3) / 4) * (kLatentDim / 64);
     e = p.num_seqs < l.workers / 4
-            ? launch_pdl(latent_merge_kernel, dim3((unsigned)pairs), dim3(128 * kMergeGroups), 0, stream, p)
-            : launch_pdl(latent_merge_warp_kernel, dim3((unsigned)((pairs + 3) / 4)), dim3(128), 0, stream, p);
+            ? launch_pdl(latent_merge_kernel<16>, dim3(tasks), dim3(32 * 16), 0, stream, p)
+            : launch_pdl(latent_merge_kernel<1>, dim3((tasks + 3) / 4), dim3(128), 0, stream, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
