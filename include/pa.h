@@ -205,9 +205,11 @@ pa_status pa_decode_append(void* out, const void* query, const void* key_new,
  * That the entries are equal is the caller's word: the table row of one member
  * is read for the whole group.  A member whose context is shorter than the
  * prefix is computed by itself from its own row, and so are the members of a
- * group in which fewer than two cover it, and prefixes in blocks of 4
- * tokens.  Bounds that decrease or leave [0, num_seqs], or a negative
- * prefix_blocks, set PA_ERRBIT_CONTEXT and nothing is shared.
+ * group in which fewer than two cover it.  Bounds that decrease or leave
+ * [0, num_seqs], or a negative prefix_blocks, set PA_ERRBIT_CONTEXT and nothing
+ * is shared.  Blocks of 4 tokens, num_groups == 0 and max_prefix_len <
+ * block_size share nothing either: the call is pa_decode then, and the groups
+ * are not read.
  *
  * Arithmetic: the suffix as pa_decode; the prefix as pa_prefill (fp16 products
  * with fp32 accumulation, softmax in fp32 with the weights rounded once to

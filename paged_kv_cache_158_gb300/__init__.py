@@ -190,9 +190,9 @@ def decode_workspace(num_seqs: int, num_heads: int, head_dim: int, max_context_l
 def _decode_shapes(out, query, key_cache, value_cache, block_tables, context_lens):
     S, H, D = query.shape
     NB, H2, B, D2 = key_cache.shape
-    if (H2, D2) != (H, D) or tuple(value_cache.shape) != tuple(key_cache.shape):
+    if H2 != H or D2 != D or value_cache.shape != key_cache.shape:
         raise ValueError("cache shape does not match query")
-    if tuple(out.shape) != (S, H, D) or block_tables.dim() != 2 or block_tables.shape[0] != S:
+    if out.shape != query.shape or block_tables.dim() != 2 or block_tables.shape[0] != S:
         raise ValueError("out / block_tables shape")
     if context_lens.shape != (S,):
         raise ValueError("context_lens shape")
@@ -518,8 +518,11 @@ def pa_slot_mapping(slot_mapping: torch.Tensor, block_tables: torch.Tensor, toke
 def _ptr_on(dev: int, t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
     """_ptr of a tensor that has to be on device `dev` (the library launches on the current one);
     one pass of cheap attribute reads, the message only where one fails."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass  # no tensor: _ptr says so
     _ptr(t, name, dtype)
     raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
 

@@ -201,9 +201,9 @@ struct SharedArgs {
   bool fp8;
 };
 size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_heads, int head_dim, int sms);
-// The plan (it also zeroes the counters), then the prefix pass.  Sets
-// dec.seq_start, and dec.inputs_ready to whether the suffix pass may run beside
-// the prefix pass.
+// The plan (it also zeroes the counters), then the prefix pass (at least one
+// group and block_size <= max_prefix_len).  Sets dec.seq_start and
+// dec.inputs_ready: the suffix pass runs beside the prefix pass.
 cudaError_t launch_shared_prefix(SharedArgs& g, cudaStream_t stream);
 // Joins prefix and suffix partials into the output.
 cudaError_t launch_shared_merge(const SharedArgs& g, cudaStream_t stream);

@@ -834,10 +834,8 @@ SharedParams params(const SharedArgs& g) {
   p.max_blocks = g.dec.max_blocks;
   p.num_blocks = g.dec.num_blocks;
   p.max_context_len = g.dec.max_context_len;
-  // Blocks of 4 tokens are half a swizzle atom: their prefixes stay in the
-  // suffix pass.
   const int mp = g.max_prefix_len / g.block_size;
-  p.max_prefix_blocks = g.block_size < 8 ? 0 : mp < g.dec.max_blocks ? mp : g.dec.max_blocks;
+  p.max_prefix_blocks = mp < g.dec.max_blocks ? mp : g.dec.max_blocks;
   p.num_counters = g.num_counters;
   p.workers = g.sms;
   p.scale_log2 = g.dec.scale_log2;
@@ -890,9 +888,9 @@ cudaError_t launch_shared_prefix(SharedArgs& g, cudaStream_t stream) {
   g.dec.seq_start = p.seq_start;
   // The prefix pass starts after the plan has ended; behind it, the suffix pass
   // finds the plan complete.
-  g.dec.inputs_ready = p.num_groups > 0 && p.max_prefix_blocks > 0;
+  g.dec.inputs_ready = true;
   const cudaError_t e = launch_pdl(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
-  if (e != cudaSuccess || p.num_groups == 0 || p.max_prefix_blocks == 0) return e;
+  if (e != cudaSuccess) return e;
   if (g.fp8)
     return g.head_dim == 64 ? launch_prefix_t<64, true>(g, p, stream) : launch_prefix_t<128, true>(g, p, stream);
   return g.head_dim == 64 ? launch_prefix_t<64, false>(g, p, stream) : launch_prefix_t<128, false>(g, p, stream);
