@@ -729,7 +729,7 @@ pa_status pa_latent_write(const void* latent, int64_t latent_stride, const void*
  * of a sequence's result may depend on the other sequences; the same call
  * gives the same bits.
  * Supported: block_size in {8, 16, 32}, num_heads <= 1024, num_blocks *
- * block_size < 2^31 - 64, and min(num_seqs, 1024) * ceil(c / 32) < 2^31 for
+ * block_size < 2^31 - 64, and min(num_seqs, 1024) * (ceil(c / 32) + 6) < 2^31 for
  * the longest context c that the table and max_context_len allow.  Batches of
  * more than 1024 sequences take a pair of launches for each 1024.
  */

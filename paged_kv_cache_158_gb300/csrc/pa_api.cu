@@ -951,7 +951,7 @@ pa_status pa_latent_decode(void* out, const void* query, const void* cache,
   const long long longest =
       std::min((long long)max_blocks_per_seq * block_size, (long long)max_context_len);
   if ((long long)std::min(num_seqs, pa::kLatentSeqsPerLaunch) *
-          ((longest + pa::kLatentTile - 1) / pa::kLatentTile) >= (1LL << 31))
+          ((longest + pa::kLatentTile - 1) / pa::kLatentTile + pa::kLatentSwitch) >= (1LL << 31))
     return PA_ERR_UNSUPPORTED;
   // 32-bit row coordinates of the copies (one past the last row included).
   if ((long long)num_blocks * block_size >= (1LL << 31) - 64 ||

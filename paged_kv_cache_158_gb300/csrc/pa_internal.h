@@ -167,6 +167,9 @@ constexpr int kRopeDim = 64;
 constexpr int kLatentRow = kLatentDim + kRopeDim;
 constexpr int kLatentTile = 32;            // tokens of a tile of the decode
 constexpr int kLatentSeqsPerLaunch = 1024;
+// Tiles that the change to another sequence costs (4 us with 128 heads, against
+// 0.6 a tile): the ranges of the SMs count them.
+constexpr int kLatentSwitch = 6;
 
 // Strides in 16-byte vectors.
 cudaError_t launch_latent_write(const void* latent, long long latent_stride, const void* rope,

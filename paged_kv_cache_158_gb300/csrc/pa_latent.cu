@@ -146,7 +146,7 @@ struct LatentParams {
   const int32_t* context_lens;
   float* ws_o;       // [slots][ceil(H / 32)][64][32 heads][8 values], 32-byte aligned
   float2* ws_ml;     // [slots][H]
-  int* cum;          // [S + 1] first tile of each sequence (for the merge)
+  int* cum;          // [S + 1] first unit of each sequence (for the merge)
   unsigned int* err;
   int seq_begin, num_seqs, num_heads, head_tiles, workers;
   int block_size, num_blocks, max_blocks, max_context_len;
@@ -165,9 +165,11 @@ __device__ __forceinline__ int context_of(const LatentParams& a, int s, bool rep
 }
 
 __device__ __forceinline__ int tiles_of(int c) { return (int)(((unsigned)c + kTile - 1) / kTile); }
+// What is cut into ranges: a sequence's tiles behind kLatentSwitch units for the
+// change to it.
+__device__ __forceinline__ int units_of(int n) { return n > 0 ? n + kLatentSwitch : 0; }
 
-// First tile of worker w of W over n tiles, and the worker of tile x.  No
-// more workers take part than there are tiles, so every one of them has some.
+// First unit of worker w of W over n units, and the worker of unit x.
 __device__ __forceinline__ int active_workers(const LatentParams& a, int n) {
   return max(1, min(a.workers, n));
 }
@@ -182,7 +184,7 @@ __device__ __forceinline__ int worker_of(int x, int W, int n) {
 // A worker's walk over its range: the next sequence with tiles and the tiles
 // of it that fall in the range.  Every warp role walks by itself.
 struct Walk {
-  int s, t, left;                // next sequence, its first tile, tiles left
+  int s, at, left;               // next sequence, its first unit, units left
   int c, n, t_begin, t_end;      // the current segment
   int cur;
   __device__ bool next(const LatentParams& a) {
@@ -190,14 +192,13 @@ struct Walk {
       cur = s;
       c = context_of(a, s, false);
       n = tiles_of(c);
-      t_begin = t;
-      t_end = min(n, t + left);
+      const int end = min(units_of(n), at + left);
+      t_begin = max(at - kLatentSwitch, 0);
+      t_end = max(end - kLatentSwitch, 0);
+      left -= end - at;
       ++s;
-      t = 0;
-      if (t_end > t_begin) {
-        left -= t_end - t_begin;
-        return true;
-      }
+      at = 0;
+      if (t_end > t_begin) return true;
     }
     return false;
   }
@@ -284,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kOffBar + 8 * kNumBars);
   volatile int* fail = reinterpret_cast<volatile int*>(sm + kOffBar + 8 * kNumBars + 4);
-  int* start = reinterpret_cast<int*>(sm + kOffBar + 8 * kNumBars + 8);  // first sequence, its first tile, tiles
+  // First sequence, its first unit, units, tiles.
+  int* start = reinterpret_cast<int*>(sm + kOffBar + 8 * kNumBars + 8);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = blockIdx.x & 1;
@@ -312,19 +314,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_launch_dependents();
-  // Tiles of every sequence and this worker's first: warp 0 scans 32 lengths
+  // Units of every sequence and this worker's first: warp 0 scans 32 lengths
   // at a time.
   if (warp == 0) {
     int total = 0;
     const bool first = blockIdx.x == 0;
     for (int b = 0; b < a.num_seqs; b += 32)
-      total += b + lane < a.num_seqs ? tiles_of(context_of(a, b + lane, first)) : 0;
+      total += b + lane < a.num_seqs ? units_of(tiles_of(context_of(a, b + lane, first))) : 0;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(kFullMask, total, o);
     const int W = active_workers(a, total);
     const int r0 = worker < W ? worker_begin(worker, W, total) : 0;
     const int r1 = worker < W ? worker_begin(worker + 1, W, total) : 0;
-    int run = 0;
+    int run = 0, tiles = 0;
     if (lane == 0) {
       start[0] = a.num_seqs;
       start[1] = 0;
@@ -333,21 +335,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     for (int b = 0; b < a.num_seqs; b += 32) {
       const int n = b + lane < a.num_seqs ? tiles_of(context_of(a, b + lane, false)) : 0;
-      int x = n;
+      const int units = units_of(n);
+      int x = units;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(kFullMask, x, o);
         if (lane >= o) x += y;
       }
-      const int c0 = run + x - n;
-      if (r1 > r0 && c0 <= r0 && r0 < c0 + n) {
+      const int c0 = run + x - units;
+      if (r1 > r0 && c0 <= r0 && r0 < c0 + units) {
         start[0] = b + lane;
         start[1] = r0 - c0;
       }
+      auto before = [&](int r) { return min(max(r - c0 - kLatentSwitch, 0), n); };  // its tiles before unit r
+      tiles += before(r1) - before(r0);
       if (first && b + lane < a.num_seqs) a.cum[b + lane] = c0;
       run += __shfl_sync(kFullMask, x, 31);
     }
     if (first && lane == 0) a.cum[a.num_seqs] = run;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) tiles += __shfl_xor_sync(kFullMask, tiles, o);
+    if (lane == 0) start[3] = tiles;
   }
   tc_fence_before();
   __syncthreads();
@@ -356,9 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(kFullMask, *tmem_slot, 0);
   Walk w;
   w.s = start[0];
-  w.t = start[1];
+  w.at = start[1];
   w.left = start[2];
-  const int n_tiles = w.left;
+  const int n_tiles = start[3];
 
   if (warp == kWarpTma) {
     // ---------------- TMA: each segment's queries, 32 heads a stage, and its tiles
@@ -850,7 +858,7 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) latent_merge_
     return;
   }
   const int W = active_workers(a, total);
-  const int w0 = worker_of(c0, W, total), n = worker_of(c1 - 1, W, total) - w0 + 1;
+  const int w0 = worker_of(c0 + kLatentSwitch, W, total), n = worker_of(c1 - 1, W, total) - w0 + 1;
   if (n <= 1) return;
   const size_t step_ml = a.num_heads, step_o = partial_at(a, 1, 0, 0);
   const float2* ml = a.ws_ml + (size_t)(s + w0) * a.num_heads + h;
