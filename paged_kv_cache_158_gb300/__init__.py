@@ -133,8 +133,10 @@ def _check(status: int, what: str) -> None:
         raise PAError(status, what)
 
 
-# The current stream's handle without building a torch.cuda.Stream around it (0.1 us against 2.9).
+# The current stream's handle without building a torch.cuda.Stream around it (0.1 us against 2.9), and
+# the current device (a CUDA tensor exists, so CUDA is up).
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _stream(stream) -> int:
@@ -571,7 +573,7 @@ def _decode_shared(out, query, key_cache, value_cache, block_tables, context_len
     G, = prefix_blocks.shape
     if group_start.shape != (G + 1,):
         raise ValueError("group_start must be [num_groups + 1] and prefix_blocks [num_groups]")
-    dev, i32, f16 = torch.cuda.current_device(), torch.int32, torch.float16
+    dev, i32, f16 = _current_device(), torch.int32, torch.float16
     fn, cache, scales = _lib.pa_decode_shared, f16, ()
     if fp8 is not None:
         fn, cache, scales = _lib.pa_decode_shared_fp8, torch.uint8, fp8
@@ -619,7 +621,7 @@ def pa_build_tables(block_tables: torch.Tensor, context_lens: torch.Tensor, quer
         raise ValueError("shape mismatch")
     if (group_start is None) != (prefix_blocks is None):
         raise ValueError("group_start and prefix_blocks go together")
-    dev, i32 = torch.cuda.current_device(), torch.int32
+    dev, i32 = _current_device(), torch.int32
     G, gs, pb = 0, None, None
     if prefix_blocks is not None:
         G, = prefix_blocks.shape
@@ -645,13 +647,11 @@ def pa_build_tables(block_tables: torch.Tensor, context_lens: torch.Tensor, quer
 
 def _rows_ptr(dev: int, t: torch.Tensor, name: str) -> int:
     """fp16 rows whose values are adjacent; the rows may be apart (a slice of a wider array)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.float16:
         raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    if t.dim() != 2 or t.stride(1) != 1:
+    if t.stride(1) != 1:
         raise ValueError(f"{name} must be [T, n] with adjacent values")
     return t.data_ptr()
 
@@ -665,7 +665,7 @@ def pa_latent_write(latent: torch.Tensor, rope: torch.Tensor, cache: torch.Tenso
     NB, B, W = cache.shape
     if T2 != T or W != L + R or slot_mapping.shape != (T,):
         raise ValueError("shape mismatch")
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     st = _lib.pa_latent_write(_rows_ptr(dev, latent, "latent"), latent.stride(0) if T > 1 else L,
                               _rows_ptr(dev, rope, "rope"), rope.stride(0) if T > 1 else R,
                               _ptr_on(dev, cache, "cache", torch.float16),
@@ -697,7 +697,7 @@ def pa_latent_decode(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor
     S3, MB = block_tables.shape
     if W2 != W or S2 != S or H2 != H or S3 != S or context_lens.shape != (S,):
         raise ValueError("shape mismatch")
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     st = _lib.pa_latent_decode(_ptr_on(dev, out, "out", torch.float16),
                                _ptr_on(dev, query, "query", torch.float16),
                                _ptr_on(dev, cache, "cache", torch.float16),
