@@ -17,9 +17,10 @@
 //  * A cluster of two CTAs takes (128 heads) x (a range of 32-token tiles): the
 //    batch's tiles, numbered sequence by sequence, are cut into equal ranges,
 //    one for each cluster, so ragged batches and single long contexts alike
-//    load every SM to within a tile.  More than 128 heads: the clusters of one
-//    worker (one for each 128 heads) walk the same range at the same time, so
-//    the rows come from HBM once and from L2 for the others.
+//    load every SM to within a tile; a change of sequence counts as six tiles.
+//    More than 128 heads: the clusters of one worker (one for each 128 heads)
+//    walk the same range at the same time, so the rows come from HBM once and
+//    from L2 for the others.
 //  * Worker w's part of sequence s is at most one segment; its partial result
 //    (m, l, o) goes to slot s + w of the workspace (along the walk either s or
 //    w grows, so the slots are distinct and there are at most S + W), and a
@@ -35,7 +36,8 @@
 //    the lanes were built first: M = 64 products take as long as M = 128 ones,
 //    and 64 sequences of 4096-8192 tokens with 128 heads took 246 us.)
 //  * The queries (fp16, 144 columns) are the A operand of Q K^T from tensor
-//    memory, so a product reads the tile's shared memory alone.
+//    memory, so a product reads the tile's shared memory alone.  They come
+//    through the stages, 32 heads in each, ahead of their segment's tiles.
 //  * A stage is 32 rows of the CTA's 256 latent values (four 64-value atoms of
 //    128-byte swizzle) and its 32 rotary ones (64-byte swizzle), copied by TMA
 //    one box a block and atom; it is the K operand of Q K^T and, its four atoms
@@ -45,7 +47,8 @@
 //    a tile's chain (product, exchange, softmax, product) takes 2 us, most of
 //    it waiting, so three tiles are on their way at a time.  (Two groups on
 //    64-token tiles: the same 64 sequences 172 us, three on 32-token ones 154;
-//    four, 160: their registers spill.)  The row's reference goes from tile to
+//    four, 160: their registers spill.  Two groups that send a tile ahead: 146
+//    against 151, but long contexts with 64 heads 59 against 56.)  The row's reference goes from tile to
 //    tile through shared memory; each group keeps the sum of its own tiles,
 //    joined at the segment's end.  References and sums are fp32, P is rounded
 //    once to fp16 (the sum adds the rounded weights).  The reference moves only
@@ -54,12 +57,16 @@
 //  * Copies, Q K^T and P V are issued by a thread each, in three warps of their
 //    own.  A segment's queries are loaded beside the epilogue of the one
 //    before.
+//  * A wait that ends at once costs a warp 55 cycles, with a vote behind it 123,
+//    with the failure flag read as well 199, and a tile has five: here a wait
+//    is one test and one vote (60 -> 56 us for two long contexts).
 //
-// Measured (inputs out of L2): 4 sequences of 16-300 tokens, 16 heads, 11 us,
+// Measured (inputs out of L2): 4 sequences of 16-300 tokens, 16 heads, 10 us,
 // most of it launches and one tile's chain; two of 60-100 thousand, 64 heads,
-// 60 us (46% of the HBM floor); 64 of 4096-8192, 128 heads, 151 us (47%).  What
-// bounds them is that chain: 0.6-0.8 us a tile in the steady state, where HBM
-// would need 0.36, and about 5 us at each change of sequence within a range.
+// 50 us (55% of the HBM floor); 64 of 4096-8192, 128 heads, 141 us (50%).  What
+// bounds them is that chain: 0.49-0.65 us a tile, where HBM would need
+// 0.36-0.43, about 3 us at each change of sequence within a range, and 10 us of
+// start and merge.
 #include <cuda.h>
 #include <cuda_fp16.h>
 

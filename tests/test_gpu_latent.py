@@ -195,6 +195,21 @@ def test_a_row_of_infinite_logits_stays_in_its_row():
     assert torch.equal(out[keep], ref[keep])
 
 
+@pytest.mark.parametrize("H", [1, 16, 40, 130])
+def test_queries_of_the_next_sequence_stay_in_it(H):
+    """A tile of 32 heads holds the rows that follow a sequence's last head: the next one's."""
+    b = Batch(H, [70, 300, 33], H, 16)
+    ref = b.run()
+    b.check(ref)
+    for bad in (float("nan"), float("inf"), -60000.0):
+        q = b.q.clone()
+        b.q[1] = bad
+        out = b.run()
+        assert torch.equal(out[0].view(torch.int16), ref[0].view(torch.int16))
+        assert torch.equal(out[2].view(torch.int16), ref[2].view(torch.int16))
+        b.q = q
+
+
 def test_clipped_lengths_and_bad_blocks_are_reported():
     b = Batch(6, [200, 100, 50], 16, 16, width=0)
     bt, ctx = b.tensors()

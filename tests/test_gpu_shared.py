@@ -248,6 +248,14 @@ def test_bad_groups_lengths_and_blocks_are_reported():
     b.check(out)
 
 
+@pytest.mark.parametrize("B,bound", [(4, 10 ** 6), (16, 15)])
+def test_groups_are_not_read_where_nothing_can_be_shared(B, bound):
+    b = Batch(28, [6, 6], [10, 20], [7, 50], 2, 64, B)
+    b.starts, b.max_prefix = np.array([5, -7, 99], dtype=np.int32), bound
+    b.check(b.run())
+    assert pa.pa_check_errors()[1] == 0
+
+
 def test_captured_and_replayed_with_new_lengths_and_groups():
     b = Batch(28, [4, 8], [20, 10], [60, 100], 4, 128, 16)
     t, ws = b.tensors(), b.workspace()
