@@ -228,6 +228,18 @@ __device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, uint32_t x, u
       : "memory");
 }
 
+// The end of a tmem_ld32, whose values are used after it.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
 // An arrival on the other CTA's barrier that orders nothing by itself.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -569,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t x_free_peer = peer_address(bar(kXFree + x), rank ^ 1);
     const unsigned char* x_own = sm + kOffX + x * kXBytes + row * 16;
     const uint32_t x_bytes = (uint32_t)live_warps * 32 * kTile * 4;
+    const int px = (x + kGroups - 1) % kGroups;
     float* ref_s = reinterpret_cast<float*>(sm + kOffRef) + row;
     float2* ml_s = reinterpret_cast<float2*>(sm + kOffMl) + row;
     auto wait = [&](int b, uint32_t parity) { return mbar_wait_warp(bar(b), parity, fail); };
@@ -628,11 +641,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       more = ahead.next(a);
       const int g_end = g + w.t_end - w.t_begin;
       float m = -INFINITY, l = 0.f;  // this group's reference and sum
-      for (int t = w.t_begin; g < g_end; ++t, ++g) {
-        if (g % 3 != x) continue;
-        const uint32_t par = (g / 3) & 1;
-        const int px = (g + 2) % 3;  // the group of the tile before, and that tile's phase
-        const uint32_t ppar = ((g - 1) / 3) & 1;
+      const int skip = (x + kGroups - g % kGroups) % kGroups;  // to this group's first tile
+      int t = w.t_begin + skip;
+      g += skip;
+      for (; g < g_end; t += kGroups, g += kGroups) {
+        const uint32_t par = (g / kGroups) & 1;
+        const uint32_t ppar = ((g - 1) / kGroups) & 1;  // the phase of the tile before, group px's
         const bool first = t == w.t_begin;
         ok = wait(kSFull + x, par);
         if (!ok) break;
@@ -640,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live) {
           tc_fence_after();
           tmem_ld32(tmem + t_lane + col_s(g), sr);
-          tmem_wait_ld();
+          tmem_wait_ld32(sr);
           tc_fence_before();
         }
         mbar_arrive(bar(kSFree + x));
@@ -649,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool rescale = false;
         if (live) {
           // This CTA's half of the logits to the other one; the other's half.
-          ok = g < 3 || mbar_wait_cluster(bar(kXFree + x), par ^ 1, fail);
+          ok = g < kGroups || mbar_wait_cluster(bar(kXFree + x), par ^ 1, fail);
           if (!ok) break;
 #pragma unroll
           for (int c = 0; c < kTile / 4; ++c)
@@ -693,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // returned: it is armed for tile g + 3 and given back.  (A release at
           // cluster scope would wait for the sends in flight as well: 0.9 us a
           // tile.)
-          if (row == 0 && g + 3 < n_tiles) mbar_arrive_expect_tx(bar(kXFull + x), x_bytes);
+          if (row == 0 && g + kGroups < n_tiles) mbar_arrive_expect_tx(bar(kXFull + x), x_bytes);
           if (lane == 0) mbar_arrive_remote(x_free_peer);
           const uint64_t neg2 = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
           float sq[4] = {0.f, 0.f, 0.f, 0.f};
@@ -728,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // This group's P is free once P.V of its tile before is done; O may be
         // rescaled once that of the other group's is, too.
-        ok = g < 3 || wait(kOFull + x, par ^ 1);
+        ok = g < kGroups || wait(kOFull + x, par ^ 1);
         if (!ok) break;
         if (live) {
           tc_fence_after();
@@ -763,13 +777,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // are done: the next segment's first ones run beside this one's epilogue.
       if (more) ok = load_queries(g + (seg + 1) * live_warps);
       const int last = g - 1;
-      ok = ok && wait(kOFull + last % 3, (last / 3) & 1);
+      ok = ok && wait(kOFull + last % kGroups, (last / kGroups) & 1);
       if (!ok) break;
       // The segment's output, a third of it by each group: to `out` when it is the
       // whole sequence, else a partial.
       if (live) {
         tc_fence_after();
-        m = ml_s[(last % 3) * kRows].x;
+        m = ml_s[(last % kGroups) * kRows].x;
         l = 0.f;
 #pragma unroll
         for (int u = 0; u < kGroups; ++u) {
