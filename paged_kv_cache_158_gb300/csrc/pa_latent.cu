@@ -47,8 +47,9 @@
 //    a tile's chain (product, exchange, softmax, product) takes 2 us, most of
 //    it waiting, so three tiles are on their way at a time.  (Two groups on
 //    64-token tiles: the same 64 sequences 172 us, three on 32-token ones 154;
-//    four, 160: their registers spill.  Two groups that send a tile ahead: 146
-//    against 151, but long contexts with 64 heads 59 against 56.)  The row's reference goes from tile to
+//    four, 160: their registers spill.  Two groups that send a tile ahead: 128.6
+//    against 129, but 120 against 112.6 with 96 heads; three that do: 150, for
+//    want of registers and stages.)  The row's reference goes from tile to
 //    tile through shared memory; each group keeps the sum of its own tiles,
 //    joined at the segment's end.  References and sums are fp32, P is rounded
 //    once to fp16 (the sum adds the rounded weights).  The reference moves only
@@ -63,10 +64,10 @@
 //
 // Measured (inputs out of L2): 4 sequences of 16-300 tokens, 16 heads, 10 us,
 // most of it launches and one tile's chain; two of 60-100 thousand, 64 heads,
-// 50 us (55% of the HBM floor); 64 of 4096-8192, 128 heads, 141 us (50%).  What
-// bounds them is that chain: 0.49-0.65 us a tile, where HBM would need
+// 48.5 us (57% of the HBM floor); 64 of 4096-8192, 128 heads, 130 us (54%).
+// What bounds them is that chain: 0.48-0.6 us a tile, where HBM would need
 // 0.36-0.43, about 3 us at each change of sequence within a range, and 10 us of
-// start and merge.
+// start and merge.  Eight stages do as well as nine (seven: 49 us, six: 51).
 #include <cuda.h>
 #include <cuda_fp16.h>
 
