@@ -217,7 +217,9 @@ pa_status pa_decode_append(void* out, const void* query, const void* key_new,
  * result rounded once to fp16.  The prefix is split among SMs by the whole
  * batch, so the last bits may depend on the other groups; the same call gives
  * the same bits.
- * num_groups <= num_seqs; num_blocks * num_heads * block_size < 2^31 - 1.
+ * num_groups <= num_seqs (else PA_ERR_INVALID_ARG); num_blocks * num_heads *
+ * block_size < 2^31 - 1 and (num_seqs / 128 + num_groups) * num_heads *
+ * (max_prefix_len / 64 + 1) < 2^31 (else PA_ERR_UNSUPPORTED).
  */
 size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int num_heads, int head_dim,
                                        int max_context_len, int max_prefix_len);
