@@ -54,6 +54,8 @@ _lib.pa_decode_partition_tokens.argtypes = [_i32, _i32, _i32]
 _lib.pa_decode_partition_tokens.restype = _i32
 _lib.pa_decode_set_partition_tokens.argtypes = [_i32]
 _lib.pa_decode_set_partition_tokens.restype = None
+_lib.pa_decode_shared_set_min_values.argtypes = [ctypes.c_int64]
+_lib.pa_decode_shared_set_min_values.restype = None
 _f32 = ctypes.c_float
 _lib.pa_decode_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
                                _f32, _f32, _f32, _i32, _vp, _sz, _vp]
@@ -179,6 +181,11 @@ def pa_decode_partition_tokens(num_seqs: int, num_heads: int, max_context_len: i
 
 def pa_decode_set_partition_tokens(tokens: int) -> None:
     _lib.pa_decode_set_partition_tokens(int(tokens))
+
+
+def pa_decode_shared_set_min_values(values: int) -> None:
+    """K and V values below which pa_decode_shared takes the plain decode (negative: the default)."""
+    _lib.pa_decode_shared_set_min_values(int(values))
 
 
 def decode_workspace(num_seqs: int, num_heads: int, head_dim: int, max_context_len: int,
@@ -738,5 +745,5 @@ __all__ = [
     "pa_decode_shared", "pa_decode_shared_fp8", "pa_decode_shared_workspace_size", "decode_shared_workspace",
     "pa_latent_write", "pa_latent_decode", "pa_latent_decode_workspace_size", "latent_decode_workspace",
     "pa_status_string", "pa_decode_workspace_size", "pa_decode_partition_tokens",
-    "pa_decode_set_partition_tokens", "decode_workspace", "raise_on_device_errors", "PAError",
+    "pa_decode_set_partition_tokens", "pa_decode_shared_set_min_values", "decode_workspace", "raise_on_device_errors", "PAError",
 ]

@@ -80,6 +80,14 @@ unsigned int* g_err_ptr[kMaxDevices];
 int g_sms[kMaxDevices];
 bool g_prepared[kMaxDevices];
 std::atomic<int> g_part_override{0};
+// K and V values that sharing spares at most, below which the plain decode is
+// taken (pa_decode_shared_set_min_values).  16 tokens a block, D = 128, fp16,
+// plain and shared in us: 8 sequences behind 1024, 32 heads (59 million) 23.3
+// and 23.6; 32 behind 1024, 8 heads (65) 23.6 and 32.0; 32 behind 256, 32 heads
+// (65) 29.1 and 26.1; 4 behind 4096, 32 heads (101) 35.1 and 30.2; 4 behind 256,
+// 32 heads (6) 10.3 and 17.6.
+constexpr long long kMinSharedValues = 64LL << 20;
+std::atomic<long long> g_min_shared{kMinSharedValues};
 
 struct DeviceState {
   unsigned int* err;
@@ -344,10 +352,13 @@ pa_status decode_shared_impl(bool fp8, void* out, const void* query, const void*
       !pa::prefill_rows_fit(num_blocks, num_heads, block_size))
     return PA_ERR_UNSUPPORTED;
   // Nothing to share (blocks of 4 tokens are half a swizzle atom: their prefixes
-  // have no pass of their own): the plain decode, which needs no plan and, for
-  // short contexts, no merge.  4 sequences, 8 heads of 64, blocks of 4: 14.2 us with
+  // have no pass of their own), or less than the passes cost: the plain decode,
+  // which needs no plan and, for short contexts, no merge.  4 sequences, 8 heads of 64, blocks of 4: 14.2 us with
   // the plan and the merge, 12.9 so.
-  if (num_groups == 0 || block_size < 8 || max_prefix_len < block_size)
+  const double spared = 2. * (num_seqs - num_groups) * num_heads * head_dim *
+                        std::min(max_prefix_len, max_context_len);
+  if (num_groups == 0 || block_size < 8 || max_prefix_len < block_size ||
+      spared < (double)g_min_shared.load(std::memory_order_relaxed))
     return decode_impl(fp8, out, query, key_cache, value_cache, block_tables, max_blocks_per_seq,
                        context_lens, num_seqs, num_heads, head_dim, block_size, num_blocks, scale,
                        k_scale, v_scale, max_context_len, workspace, workspace_bytes, 0u, stream);
@@ -462,6 +473,10 @@ int pa_decode_partition_tokens(int num_seqs, int num_heads, int max_context_len)
 
 void pa_decode_set_partition_tokens(int tokens) {
   g_part_override.store(tokens > 0 ? tokens : 0, std::memory_order_relaxed);
+}
+
+void pa_decode_shared_set_min_values(int64_t values) {
+  g_min_shared.store(values >= 0 ? values : kMinSharedValues, std::memory_order_relaxed);
 }
 
 size_t pa_decode_workspace_size(int num_seqs, int num_heads, int head_dim, int max_context_len) {

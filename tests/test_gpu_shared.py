@@ -30,9 +30,11 @@ KS, VS = 0.0137, 0.0119
 @pytest.fixture(autouse=True)
 def _clean():
     pa.pa_decode_set_partition_tokens(0)
+    pa.pa_decode_shared_set_min_values(0)      # these batches are small: share all the same
     pa.pa_check_errors()
     yield
     pa.pa_decode_set_partition_tokens(0)
+    pa.pa_decode_shared_set_min_values(-1)
     torch.cuda.synchronize()
 
 
@@ -246,6 +248,30 @@ def test_bad_groups_lengths_and_blocks_are_reported():
     assert pa.pa_check_errors()[1] == pa.PA_ERRBIT_CONTEXT
     b.ctx[2] = 0
     b.check(out)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp16", "fp8"])
+def test_small_batches_are_decoded_plainly(fp8):
+    """Below 2^26 spared K and V values the bits are the plain decode's; from there on the prefix
+    has its own pass, and the groups are read."""
+    b = Batch(29, [9], [16], [30, 5], 4, 64, 16, fp8)
+    spared = 2 * 8 * 4 * 64 * 256
+    t = b.tensors()
+    ref = torch.empty_like(b.run(t=t))
+    if fp8:
+        pa.pa_decode_fp8(ref, b.q, b.k, b.v, t[0], t[1], b.scale, KS, VS, b.max_len,
+                         pa.decode_workspace(b.S, b.H, b.D, b.max_len))
+    else:
+        pa.pa_decode(ref, b.q, b.k, b.v, t[0], t[1], b.scale, b.max_len,
+                     pa.decode_workspace(b.S, b.H, b.D, b.max_len))
+    bad = (t[0], t[1], torch.tensor([4, 2], dtype=torch.int32, device=DEV), t[3])
+    for values, plain in ((-1, True), (spared + 1, True), (spared, False), (0, False)):
+        pa.pa_decode_shared_set_min_values(values)
+        out = b.run(t=t)
+        b.check(out)
+        assert not plain or torch.equal(out.view(torch.int16), ref.view(torch.int16))
+        b.check(b.run(t=bad))
+        assert pa.pa_check_errors()[1] == (0 if plain else pa.PA_ERRBIT_CONTEXT)
 
 
 @pytest.mark.parametrize("B,bound", [(4, 10 ** 6), (16, 15)])
