@@ -210,7 +210,7 @@ pa_status pa_decode_append(void* out, const void* query, const void* key_new,
  * is shared.  Blocks of 4 tokens, num_groups == 0 and max_prefix_len <
  * block_size share nothing either, and small batches gain nothing by it
  * (2 * (num_seqs - num_groups) * num_heads * head_dim * min(max_prefix_len,
- * max_context_len) below 2^26, the K and V values spared at most): the call
+ * max_context_len) below 3 * 2^24, the K and V values spared at most): the call
  * is pa_decode then, and the groups are not read.
  *
  * Arithmetic: the suffix as pa_decode; the prefix as pa_prefill (fp16 products
@@ -791,7 +791,7 @@ void pa_decode_set_partition_tokens(int tokens);
 
 /*
  * Process-wide override of the number of K and V values below which
- * pa_decode_shared takes the plain decode (negative: the default, 2^26; 0:
+ * pa_decode_shared takes the plain decode (negative: the default, 3 * 2^24; 0:
  * never by size).  Meant for tuning and for tests of small shared batches.
  */
 void pa_decode_shared_set_min_values(int64_t values);

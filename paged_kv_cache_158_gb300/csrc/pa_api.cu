@@ -82,11 +82,11 @@ bool g_prepared[kMaxDevices];
 std::atomic<int> g_part_override{0};
 // K and V values that sharing spares at most, below which the plain decode is
 // taken (pa_decode_shared_set_min_values).  16 tokens a block, D = 128, fp16,
-// plain and shared in us: 8 sequences behind 1024, 32 heads (59 million) 23.3
-// and 23.6; 32 behind 1024, 8 heads (65) 23.6 and 32.0; 32 behind 256, 32 heads
-// (65) 29.1 and 26.1; 4 behind 4096, 32 heads (101) 35.1 and 30.2; 4 behind 256,
-// 32 heads (6) 10.3 and 17.6.
-constexpr long long kMinSharedValues = 64LL << 20;
+// plain and shared in us: 4 sequences behind 256, 32 heads (6 million) 10.3 and
+// 16.0; 64 behind 256, 8 heads (33) 19.8 and 21.3; 8 behind 4096, 8 heads (59)
+// 24.4 and 24.8; 8 behind 1024, 32 heads (59) 23.2 and 21.7; 32 behind 1024, 8
+// heads (65) 23.5 and 20.1; 32 behind 256, 32 heads (65) 29.3 and 21.4.
+constexpr long long kMinSharedValues = 48LL << 20;
 std::atomic<long long> g_min_shared{kMinSharedValues};
 
 struct DeviceState {

@@ -21,7 +21,7 @@
 //    position, each group's tiles and their running sum go to the workspace.
 //  * Prefix (one persistent CTA per SM): units are (group, 128 members, head);
 //    the tiles of all units are numbered in that order and cut into equal
-//    ranges, so few groups with long prefixes load every SM alike.  A worker's
+//    ranges (of at least four), so few groups with long prefixes load every SM alike.  A worker's
 //    part of a unit is one segment; its rows go to partial rows
 //    2 H s0 + h * rows + 128 w (s0: the unit's first sequence; w: the worker;
 //    rows: the unit's, copies counted, at most two for a member), distinct
@@ -48,8 +48,8 @@
 //
 // Measured (D = 128, inputs out of L2), with the floor of the distinct bytes in
 // brackets: 64 sequences behind 512 tokens with 1-1536 of their own, 32 heads,
-// fp16: 134 us (122); 128 behind 8192 with 1-512: 119 us (101); 95 in five
-// groups behind 1000-5000 with 0-700, 40 heads, E4M3: 118 us (74).  The first
+// fp16: 130 us (122); 128 behind 8192 with 1-512: 119 us (101); 95 in five
+// groups behind 1000-5000 with 0-700, 40 heads, E4M3: 117 us (74).  The first
 // two wait for HBM; with half the bytes, the third for the softmax of its
 // prefix tiles and for the suffix CTAs' issue slots.
 #include <cuda.h>
@@ -227,8 +227,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
 
 // ---- prefix pass ----------------------------------------------------------------
 
+// Workers for n tiles: at least four tiles each, since every segment's partial
+// rows are merged (32 sequences behind 1024 tokens, 8 heads: 32 us with one
+// tile each, 23 with two, 21 with four, 24 with six).
 __device__ __forceinline__ int active_workers(const SharedParams& a, int n) {
-  return max(1, min(a.workers, n));
+  return max(1, min(a.workers, n / 4));
 }
 __device__ __forceinline__ int worker_begin(int w, int W, int n) { return (int)((long long)w * n / W); }
 __device__ __forceinline__ int worker_of(int x, int W, int n) {
@@ -767,7 +770,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams a)
     for (int o = 16; o >= 1; o >>= 1) wl += __shfl_xor_sync(kFullMask, wl, o);
     L += wl;
     const int cnt = min(32, n - base);
-#pragma unroll 4
+#pragma unroll 8  // their loads on their way together
     for (int j = 0; j < cnt; ++j) {
       const int i = base + j;
       const float* src = (i < n_pre ? a.pre_o + pre_row(i) * D

@@ -252,7 +252,7 @@ def test_bad_groups_lengths_and_blocks_are_reported():
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["fp16", "fp8"])
 def test_small_batches_are_decoded_plainly(fp8):
-    """Below 2^26 spared K and V values the bits are the plain decode's; from there on the prefix
+    """Below 3 * 2^24 spared K and V values the bits are the plain decode's; from there on the prefix
     has its own pass, and the groups are read."""
     b = Batch(29, [9], [16], [30, 5], 4, 64, 16, fp8)
     spared = 2 * 8 * 4 * 64 * 256
