@@ -178,8 +178,10 @@ __device__ __forceinline__ int tiles_of(int c) { return (int)(((unsigned)c + kTi
 __device__ __forceinline__ int units_of(int n) { return n > 0 ? n + kLatentSwitch : 0; }
 
 // First unit of worker w of W over n units, and the worker of unit x.
+// At least two units a worker: single tiles leave more partials than they save
+// time (4 sequences of 60 tokens, 128 heads: 20 us with one, 15 with two).
 __device__ __forceinline__ int active_workers(const LatentParams& a, int n) {
-  return max(1, min(a.workers, n));
+  return max(1, min(a.workers, n / 2));
 }
 __device__ __forceinline__ int worker_begin(int w, int W, int n) {
   return (int)((long long)w * n / W);
@@ -1041,8 +1043,12 @@ cudaError_t launch_latent_decode(const LatentArgs& g, cudaStream_t stream) {
     e = launch_pdl_cluster(latent_decode_kernel, dim3((unsigned)(2 * l.workers * l.head_tiles)),
                            dim3(kThreads), 2, kSmem, stream, tc, tr, tq, tqr, p);
     if (e != cudaSuccess) return e;
+    // CTAs of 16 warps a task only where tasks are few and segments many.  In us,
+    // 16 warps and one: 2 sequences of 3000 tokens, 128 heads (512 tasks, 38
+    // segments) 19.2 and 27.5; 16 of 300, 16 heads (512 tasks, 5) 14.8 and 11.8;
+    // 8 of 20 thousand, 128 heads (2048 tasks, 9) 73 and 57.
     const unsigned tasks = (unsigned)p.num_seqs * ((p.num_heads + 3) / 4) * (kLatentDim / 64);
-    e = p.num_seqs < l.workers / 4
+    e = tasks <= 512 && p.num_seqs <= l.workers / 8
             ? launch_pdl(latent_merge_kernel<16>, dim3(tasks), dim3(32 * 16), 0, stream, p)
             : launch_pdl(latent_merge_kernel<1>, dim3((tasks + 3) / 4), dim3(128), 0, stream, p);
     if (e != cudaSuccess) return e;
